@@ -23,7 +23,8 @@ PROBE_SOURCES = ["probe.hip"]
 PROBE_LIB = os.path.join(HERE, "libgemm_probe.so")
 ARCH = "gfx950"
 
-SOURCES = ["gemm_api.hip", "splitk.hip", "sgemm_dl.hip", "sgemm_mfma.hip", "hgemm_mfma.hip", "hgemm_tr.hip", "sgemm_simt.hip"]
+SOURCES = ["gemm_api.hip", "splitk.hip", "sgemm_dl.hip", "sgemm_mfma.hip", "hgemm_mfma.hip", "hgemm_tr.hip", "sgemm_simt.hip",
+           "mx_api.hip", "mx_quant.hip", "mx_matmul.hip", "mx_wgrad.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "gemm_internal.h"
+#include "mx_internal.h"
 
 namespace gemm {
 
@@ -856,6 +857,12 @@ gemm_status_t run_splitk_static(int dtype, int64_t M, int64_t N, int64_t K, cons
 }
 
 }  // namespace
+
+gemm_status_t set_last_error(gemm_status_t st, const char* msg) {
+  snprintf(g_err, sizeof(g_err), "%s", msg);
+  return st;
+}
+
 }  // namespace gemm
 
 using namespace gemm;

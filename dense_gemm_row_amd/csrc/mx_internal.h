@@ -1,0 +1,83 @@
+// Internal declarations of the microscaled operators (include/gemm_mx.h):
+// kernel arguments, the launch functions of mx_quant.hip, mx_matmul.hip and
+// mx_wgrad.hip, and the error hook of the C-ABI layer.
+#pragma once
+
+#include "gemm_internal.h"
+#include "gemm_mx.h"
+
+namespace gemm {
+
+// gemm_last_error()'s message for the calling thread ("" clears it); returns
+// st.  Defined in gemm_api.hip.
+gemm_status_t set_last_error(gemm_status_t st, const char* msg);
+
+namespace mx {
+
+constexpr int BLOCK = 32;  // elements per scale
+
+// A coded matrix: rows of whole blocks (see gemm_mx.h).
+struct Coded {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t ldq, lds;
+};
+
+struct QuantArgs {
+  const void* X;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t ldx, ldq, lds;
+  int rows, cols;  // of X
+};
+
+struct DequantArgs {
+  Coded q;
+  void* X;
+  int64_t ldx;
+  int rows, cols;  // of X
+};
+
+struct MatmulArgs {
+  Coded a, b;
+  void* C;
+  int64_t ldc;
+  int M, N, K;
+  Epi epi;
+};
+
+struct WgradArgs {
+  Coded x;
+  const void* dY;
+  void* dW;
+  float* partial;  // S planes of F x N, or null
+  int64_t ldy, ldw;
+  int T, F, N;
+  int splits, chunk;  // token chunk of each split (a multiple of 32)
+  float alpha, beta;
+};
+
+hipError_t launch_quantize(int dtype, int format, bool trans, const QuantArgs& a, hipStream_t s);
+hipError_t launch_dequantize(int dtype, int format, bool trans, const DequantArgs& a, hipStream_t s);
+hipError_t launch_matmul(int c_dtype, const MatmulArgs& a, hipStream_t s);
+hipError_t launch_wgrad(int y_dtype, int c_dtype, const WgradArgs& a, hipStream_t s);
+// Token chunks of gemm_mx_wgrad with an unlimited workspace (1: not split).
+int wgrad_splits(int y_dtype, int64_t T, int64_t F, int64_t N, int* chunk);
+
+// Output types as template arguments: GEMM_DTYPE_F32 / _F16 / _BF16.
+template <int DT>
+struct TypeOf;
+template <>
+struct TypeOf<GEMM_DTYPE_F32> { typedef float type; };
+template <>
+struct TypeOf<GEMM_DTYPE_F16> { typedef _Float16 type; };
+template <>
+struct TypeOf<GEMM_DTYPE_BF16> { typedef __bf16 type; };
+
+// The FP32 factor of a scale byte as the conversion instructions take it:
+// they read its exponent field alone (0 gives 2^-127, 255 gives NaN values;
+// both checked on the device).
+__device__ __forceinline__ float scale_float(unsigned byte) { return __builtin_bit_cast(float, byte << 23); }
+
+}  // namespace mx
+}  // namespace gemm
