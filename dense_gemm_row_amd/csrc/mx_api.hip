@@ -150,9 +150,7 @@ gemm_status_t gemm_mx_matmul(int32_t c_dtype, int64_t M, int64_t N, int64_t K, c
 
 int64_t gemm_mx_wgrad_workspace_bytes(int32_t y_dtype, int64_t T, int64_t F, int64_t N) {
   if (!float_dtype(y_dtype) || !size_ok(T) || !size_ok(F) || !size_ok(N)) return -1;
-  int chunk;
-  const int s = wgrad_splits(y_dtype, T, F, N, &chunk);
-  return s > 1 ? (int64_t)s * F * N * 4 : 0;
+  return wgrad_plan(y_dtype, T, F, N).bytes();
 }
 
 gemm_status_t gemm_mx_wgrad(int32_t y_dtype, int32_t c_dtype, int64_t T, int64_t F, int64_t N, const uint8_t* codes,
@@ -170,18 +168,15 @@ gemm_status_t gemm_mx_wgrad(int32_t y_dtype, int32_t c_dtype, int64_t T, int64_t
   if ((st = check_dense("dY", dY, T, N, ldy, dtype_bytes(y_dtype), &y)) != GEMM_OK) return st;
   if ((st = check_dense("dW", dW, F, N, ldw, dtype_bytes(c_dtype), &w)) != GEMM_OK) return st;
   if (overlap(w, c) || overlap(w, s) || overlap(w, y)) return fail(GEMM_ERR_ALIAS, "dW overlaps an operand");
-  WgradArgs p{{codes, scales, ldq, lds}, dY, dW, nullptr, ldy, ldw, (int)T, (int)F, (int)N, 1, (int)T, alpha, beta};
-  int chunk;
-  const int splits = wgrad_splits(y_dtype, T, F, N, &chunk);
-  const int64_t need = splits > 1 ? (int64_t)splits * F * N * 4 : 0;
+  WgradArgs p{{codes, scales, ldq, lds}, dY, dW, ldy, ldw, (int)T, (int)F, (int)N, alpha, beta, nullptr, 0};
+  const int64_t need = wgrad_plan(y_dtype, T, F, N).bytes();
   if (need > 0 && workspace && workspace_bytes >= need) {
     if ((uintptr_t)workspace % 16 != 0) return fail(GEMM_ERR_INVALID_ARG, "workspace not 16-byte aligned");
     const Span k = span(workspace, 1, need, need);
     if (overlap(k, c) || overlap(k, s) || overlap(k, y) || overlap(k, w))
       return fail(GEMM_ERR_ALIAS, "workspace overlaps an operand");
-    p.partial = static_cast<float*>(workspace);
-    p.splits = splits;
-    p.chunk = chunk;
+    p.workspace = workspace;
+    p.workspace_bytes = need;
   }
   return launched(launch_wgrad(y_dtype, c_dtype, p, static_cast<hipStream_t>(stream)));
 }

@@ -50,19 +50,28 @@ struct WgradArgs {
   Coded x;
   const void* dY;
   void* dW;
-  float* partial;  // S planes of F x N, or null
   int64_t ldy, ldw;
   int T, F, N;
-  int splits, chunk;  // token chunk of each split (a multiple of 32)
   float alpha, beta;
+  void* workspace;  // 16-byte aligned, or null
+  int64_t workspace_bytes;
+};
+
+// How a weight gradient runs on the pipelined kernel.  The workspace holds
+// dY's bfloat16 terms (`planes` bytes: where dY is not bfloat16 or has rows
+// of another length than whole 16 bytes), then the splits' FP32 sums.
+struct WgradPlan {
+  int tile = 0;     // 0: the general kernel
+  int splits = 1, chunk = 0;  // tokens of a split, a multiple of 128
+  int64_t planes = 0, partials = 0;
+  int64_t bytes() const { return planes + partials; }
 };
 
 hipError_t launch_quantize(int dtype, int format, bool trans, const QuantArgs& a, hipStream_t s);
 hipError_t launch_dequantize(int dtype, int format, bool trans, const DequantArgs& a, hipStream_t s);
 hipError_t launch_matmul(int c_dtype, const MatmulArgs& a, hipStream_t s);
 hipError_t launch_wgrad(int y_dtype, int c_dtype, const WgradArgs& a, hipStream_t s);
-// Token chunks of gemm_mx_wgrad with an unlimited workspace (1: not split).
-int wgrad_splits(int y_dtype, int64_t T, int64_t F, int64_t N, int* chunk);
+WgradPlan wgrad_plan(int y_dtype, int64_t T, int64_t F, int64_t N);
 
 // Output types as template arguments: GEMM_DTYPE_F32 / _F16 / _BF16.
 template <int DT>

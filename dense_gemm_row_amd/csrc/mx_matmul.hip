@@ -342,6 +342,12 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
   const int rows = p.M - (m0 + wm0), cols = p.N - (n0 + wn0);
   const Out* C = static_cast<Out*>(p.C) + (int64_t)(m0 + wm0) * p.ldc + (n0 + wn0);
   auto store = [&](auto VEC) __attribute__((always_inline)) {
+    f32x4 bias[NB];
+    if constexpr (EPI) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) bias[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (p.epi.bias) load_block_row<GEMM_DTYPE_F32, NB, false>(p.epi.bias + n0 + wn0, 0u, cols, bias, q);
+    }
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       const int m = 16 * i + r;
@@ -350,16 +356,14 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) v[j] = acc[j][i];
       if constexpr (EPI) {
+        f32x4 old[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) old[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (p.epi.beta != 0.f) load_block_row<DT, NB, decltype(VEC)::value>(C, row, cols, old, q);
 #pragma unroll
         for (int j = 0; j < NB; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int n = 16 * j + 4 * q + e;
-            if (m < rows && n < cols) {
-              const float old = p.epi.beta != 0.f ? (float)C[m * p.ldc + n] : 0.f;
-              v[j][e] = epi_value(p.epi, v[j][e], old, p.epi.bias ? p.epi.bias[n0 + wn0 + n] : 0.f);
-            }
-          }
+          for (int e = 0; e < 4; ++e) v[j][e] = epi_value(p.epi, v[j][e], old[j][e], bias[j][e]);
       }
       store_block_row<DT, NB, decltype(VEC)::value>(C, row, cols, v, q);
     }

@@ -103,9 +103,11 @@ __device__ __forceinline__ void store_block_row(const void* C, unsigned row, int
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v[nb]), rc, off, 0, 2);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, (float)v[nb][i]), rc,
+        for (int i = 0; i < 4; ++i) {
+          const float x = v[nb][i];  // (a vector's element bit-cast in place is its first)
+          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), rc,
                                                 n + i < cols ? row + (n + i) * es : OOB, 0, 0);
+        }
       }
     }
   } else {
@@ -131,6 +133,40 @@ __device__ __forceinline__ void store_block_row(const void* C, unsigned row, int
         for (int i = 0; i < 8; ++i)
           __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(w[i / 2] >> (16 * (i % 2))), rc,
                                                 n + i < cols ? row + (n + i) * es : OOB, 0, 0);
+      }
+    }
+  }
+#endif
+}
+
+// The old values of the same block row (zeros outside), in the accumulators'
+// layout.  Branch-free like the stores: divergent branches between the
+// accumulators' uses make the register allocator move them about under a
+// partial execution mask.
+template <int DT, int NB, bool VEC>
+__device__ __forceinline__ void load_block_row(const void* C, unsigned row, int cols, f32x4 (&v)[NB], int q) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef typename TypeOf<DT>::type T;
+  constexpr unsigned es = sizeof(T);
+  const __amdgpu_buffer_rsrc_t rc = make_rsrc(C, 0x7fffffff);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int n = 16 * nb + 4 * q;
+    if constexpr (VEC && es == 4) {
+      v[nb] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, n < cols ? row + n * es : OOB, 0, 0));
+    } else if constexpr (VEC) {
+      typedef T t4 __attribute__((ext_vector_type(4)));
+      const t4 t = __builtin_bit_cast(t4, __builtin_amdgcn_raw_buffer_load_b64(rc, n < cols ? row + n * es : OOB, 0, 0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[nb][i] = (float)t[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned off = n + i < cols ? row + (n + i) * es : OOB;
+        if constexpr (es == 4)
+          v[nb][i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rc, off, 0, 0));
+        else
+          v[nb][i] = (float)__builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(rc, off, 0, 0));
       }
     }
   }

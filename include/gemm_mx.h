@@ -106,10 +106,13 @@ gemm_status_t gemm_mx_matmul(int32_t c_dtype, int64_t M, int64_t N, int64_t K,
  * FP32 as the sum of three.  Accumulated in FP32, rounded once.  beta == 0:
  * dW is not read.  T == 0: the empty sum.
  *
- * Few outputs with many tokens are split over tokens: S chunks' FP32 sums go
- * to `workspace` (gemm_mx_wgrad_workspace_bytes bytes, 16-byte aligned, not
- * overlapping the operands) and are added in chunk order.  The workspace may
- * be NULL, or smaller than that: then nothing is split.
+ * `workspace` (gemm_mx_wgrad_workspace_bytes bytes, 16-byte aligned, not
+ * overlapping the operands) takes two things: dY's bfloat16 terms, where dY
+ * is not bfloat16 or N is no multiple of 8, and, where few outputs have many
+ * tokens, the FP32 sums of S chunks of tokens, which are added in chunk
+ * order.  The workspace may be NULL, or smaller than that: then a slower
+ * kernel runs that needs none (as for a dY of rows that are not 16-byte
+ * aligned though N is a multiple of 8, or scales off 4-byte words).
  */
 gemm_status_t gemm_mx_wgrad(int32_t y_dtype, int32_t c_dtype, int64_t T, int64_t F, int64_t N,
                             const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t lds,
@@ -117,7 +120,7 @@ gemm_status_t gemm_mx_wgrad(int32_t y_dtype, int32_t c_dtype, int64_t T, int64_t
                             float alpha, float beta,
                             void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Workspace of the split above (0: not split); -1 for an unknown type or a
+/* Bytes of that workspace (0: none is used); -1 for an unknown type or a
  * size that gemm_mx_wgrad refuses. */
 int64_t gemm_mx_wgrad_workspace_bytes(int32_t y_dtype, int64_t T, int64_t F, int64_t N);
 
