@@ -78,6 +78,34 @@ gemm_status_t check_format(int dtype, int format) {
   return GEMM_OK;
 }
 
+// Scale rows of whole 4-byte words, as the pipelined product takes them.
+int64_t scale_row(int64_t cols) { return (blocks_of(cols) + 3) / 4 * 4; }
+
+// What both products share: sizes, Bt, C and the epilogue.
+gemm_status_t check_product(int c_dtype, int64_t M, int64_t N, int64_t K, const uint8_t* Bt, int64_t ldbt, const uint8_t* Bs,
+                            int64_t ldbs, void* C, int64_t ldc, const gemm_epilogue_t* epi, MatmulArgs* p, Span* c) {
+  if (!float_dtype(c_dtype)) return fail(GEMM_ERR_INVALID_ARG, "type %d is not F32, F16 or BF16", c_dtype);
+  if (!size_ok(M) || !size_ok(N) || !size_ok(K)) return fail(GEMM_ERR_INVALID_ARG, "size below 0 or above 2^31-1");
+  if (epi && epi->act != GEMM_ACT_NONE && epi->act != GEMM_ACT_RELU)
+    return fail(GEMM_ERR_INVALID_ARG, "unknown activation %d", epi->act);
+  gemm_status_t st;
+  Span b, bs;
+  if ((st = check_coded("Bt", GEMM_MX_E2M1, Bt, Bs, N, K, ldbt, ldbs, &b, &bs)) != GEMM_OK) return st;
+  if ((st = check_dense("C", C, M, N, ldc, dtype_bytes(c_dtype), c)) != GEMM_OK) return st;
+  if (overlap(*c, b) || overlap(*c, bs)) return fail(GEMM_ERR_ALIAS, "C overlaps an operand");
+  *p = MatmulArgs{{}, {Bt, Bs, ldbt, ldbs}, C, ldc, (int)M, (int)N, (int)K, Epi()};
+  if (epi) {
+    p->epi.on = true;
+    p->epi.alpha = epi->alpha;
+    p->epi.beta = epi->beta;
+    p->epi.bias = epi->bias;
+    p->epi.act = epi->act;
+    if ((uintptr_t)epi->bias % 4 != 0) return fail(GEMM_ERR_UNSUPPORTED, "bias is not aligned to its elements");
+    if (overlap(*c, span(epi->bias, epi->bias ? 1 : 0, 4 * N, 4 * N))) return fail(GEMM_ERR_ALIAS, "C overlaps the bias");
+  }
+  return GEMM_OK;
+}
+
 }  // namespace
 }  // namespace mx
 }  // namespace gemm
@@ -124,28 +152,54 @@ gemm_status_t gemm_mx_matmul(int32_t c_dtype, int64_t M, int64_t N, int64_t K, c
                              const uint8_t* As, int64_t ldas, const uint8_t* Bt, int64_t ldbt, const uint8_t* Bs,
                              int64_t ldbs, void* C, int64_t ldc, void* stream, const gemm_epilogue_t* epi) {
   set_last_error(GEMM_OK, "");
-  if (!float_dtype(c_dtype)) return fail(GEMM_ERR_INVALID_ARG, "type %d is not F32, F16 or BF16", c_dtype);
-  if (!size_ok(M) || !size_ok(N) || !size_ok(K)) return fail(GEMM_ERR_INVALID_ARG, "size below 0 or above 2^31-1");
-  if (epi && epi->act != GEMM_ACT_NONE && epi->act != GEMM_ACT_RELU)
-    return fail(GEMM_ERR_INVALID_ARG, "unknown activation %d", epi->act);
-  gemm_status_t st;
-  Span a, as, b, bs, c;
+  MatmulArgs p;
+  Span c, a, as;
+  gemm_status_t st = check_product(c_dtype, M, N, K, Bt, ldbt, Bs, ldbs, C, ldc, epi, &p, &c);
+  if (st != GEMM_OK) return st;
   if ((st = check_coded("A", GEMM_MX_E2M1, A, As, M, K, lda, ldas, &a, &as)) != GEMM_OK) return st;
-  if ((st = check_coded("Bt", GEMM_MX_E2M1, Bt, Bs, N, K, ldbt, ldbs, &b, &bs)) != GEMM_OK) return st;
-  if ((st = check_dense("C", C, M, N, ldc, dtype_bytes(c_dtype), &c)) != GEMM_OK) return st;
-  if (overlap(c, a) || overlap(c, as) || overlap(c, b) || overlap(c, bs))
-    return fail(GEMM_ERR_ALIAS, "C overlaps an operand");
-  MatmulArgs p{{A, As, lda, ldas}, {Bt, Bs, ldbt, ldbs}, C, ldc, (int)M, (int)N, (int)K, Epi()};
-  if (epi) {
-    p.epi.on = true;
-    p.epi.alpha = epi->alpha;
-    p.epi.beta = epi->beta;
-    p.epi.bias = epi->bias;
-    p.epi.act = epi->act;
-    if ((uintptr_t)epi->bias % 4 != 0) return fail(GEMM_ERR_UNSUPPORTED, "bias is not aligned to its elements");
-    if (overlap(c, span(epi->bias, epi->bias ? 1 : 0, 4 * N, 4 * N))) return fail(GEMM_ERR_ALIAS, "C overlaps the bias");
-  }
+  if (overlap(c, a) || overlap(c, as)) return fail(GEMM_ERR_ALIAS, "C overlaps an operand");
+  p.a = Coded{A, As, lda, ldas};
   return launched(launch_matmul(c_dtype, p, static_cast<hipStream_t>(stream)));
+}
+
+int64_t gemm_mx_matmul_values_workspace_bytes(int64_t M, int64_t K) {
+  if (!size_ok(M) || !size_ok(K)) return -1;
+  return M * (blocks_of(K) * 16 + scale_row(K));
+}
+
+gemm_status_t gemm_mx_matmul_values(int32_t a_dtype, int32_t c_dtype, int64_t M, int64_t N, int64_t K, const void* X,
+                                    int64_t ldx, const uint8_t* Bt, int64_t ldbt, const uint8_t* Bs, int64_t ldbs,
+                                    void* C, int64_t ldc, void* workspace, int64_t workspace_bytes, void* stream,
+                                    const gemm_epilogue_t* epi) {
+  set_last_error(GEMM_OK, "");
+  if (!float_dtype(a_dtype)) return fail(GEMM_ERR_INVALID_ARG, "type %d is not F32, F16 or BF16", a_dtype);
+  if (workspace_bytes < 0) return fail(GEMM_ERR_INVALID_ARG, "negative workspace size");
+  MatmulArgs p;
+  Span c, x;
+  gemm_status_t st = check_product(c_dtype, M, N, K, Bt, ldbt, Bs, ldbs, C, ldc, epi, &p, &c);
+  if (st != GEMM_OK) return st;
+  if ((st = check_dense("X", X, M, K, ldx, dtype_bytes(a_dtype), &x)) != GEMM_OK) return st;
+  if (overlap(c, x)) return fail(GEMM_ERR_ALIAS, "C overlaps X");
+  if (M == 0 || N == 0) return GEMM_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  p.X = X;
+  p.ldx = ldx;
+  if (M <= kValueRows && values_fit(a_dtype, p)) return launched(launch_matmul_values(a_dtype, c_dtype, p, s));
+  const int64_t need = gemm_mx_matmul_values_workspace_bytes(M, K);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return fail(GEMM_ERR_INVALID_ARG, "the workspace takes %lld bytes", (long long)need);
+    if ((uintptr_t)workspace % 16 != 0) return fail(GEMM_ERR_INVALID_ARG, "workspace not 16-byte aligned");
+    const Span k = span(workspace, 1, need, need);
+    if (overlap(k, x) || overlap(k, c) || overlap(k, span(Bt, N, row_bytes(GEMM_MX_E2M1, K), ldbt)) ||
+        overlap(k, span(Bs, N, blocks_of(K), ldbs)) ||
+        (epi && overlap(k, span(epi->bias, epi->bias ? 1 : 0, 4 * N, 4 * N))))
+      return fail(GEMM_ERR_ALIAS, "workspace overlaps an operand");
+  }
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  const QuantArgs q{X, codes, codes + M * blocks_of(K) * 16, ldx, blocks_of(K) * 16, scale_row(K), (int)M, (int)K};
+  p.a = Coded{q.codes, q.scales, q.ldq, q.lds};
+  const hipError_t e = launch_quantize(a_dtype, GEMM_MX_E2M1, false, q, s);
+  return launched(e != hipSuccess ? e : launch_matmul(c_dtype, p, s));
 }
 
 int64_t gemm_mx_wgrad_workspace_bytes(int32_t y_dtype, int64_t T, int64_t F, int64_t N) {

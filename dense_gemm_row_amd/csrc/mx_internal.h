@@ -44,6 +44,9 @@ struct MatmulArgs {
   int64_t ldc;
   int M, N, K;
   Epi epi;
+  // A as values (launch_matmul_values): rows of ldx.
+  const void* X = nullptr;
+  int64_t ldx = 0;
 };
 
 struct WgradArgs {
@@ -70,6 +73,10 @@ struct WgradPlan {
 hipError_t launch_quantize(int dtype, int format, bool trans, const QuantArgs& a, hipStream_t s);
 hipError_t launch_dequantize(int dtype, int format, bool trans, const DequantArgs& a, hipStream_t s);
 hipError_t launch_matmul(int c_dtype, const MatmulArgs& a, hipStream_t s);
+// The same with A = X quantised on the way, for what values_fit takes.
+constexpr int kValueRows = 16;
+bool values_fit(int a_dtype, const MatmulArgs& a);
+hipError_t launch_matmul_values(int a_dtype, int c_dtype, const MatmulArgs& a, hipStream_t s);
 hipError_t launch_wgrad(int y_dtype, int c_dtype, const WgradArgs& a, hipStream_t s);
 WgradPlan wgrad_plan(int y_dtype, int64_t T, int64_t F, int64_t N);
 

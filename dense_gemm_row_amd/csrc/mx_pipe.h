@@ -77,6 +77,19 @@ __device__ __forceinline__ void mfma_guard() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// The accumulators as values known in their registers at this point: what
+// precedes it wrote them, what follows reads them.  A guard alone is no
+// fence for them (the compiler read results ahead of it).
+template <int NB, int MB>
+__device__ __forceinline__ void pin(f32x4 (&acc)[NB][MB]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int i = 0; i < MB; ++i) asm volatile("" : "+a"(acc[j][i]));
+#endif
+}
+
 // Stores of one 16-row block row of a wave's tile, through a buffer over C
 // (so without branches: what lies outside the matrix gets an offset past
 // the range).  Block nb's register i of lane l is element (l%16, 16nb +

@@ -323,12 +323,8 @@ wgrad_pipe(PipeArgs p, TileMap map, int vec) {
 #pragma unroll
   for (int j = 0; j < NB; ++j)
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#if defined(__HIP_DEVICE_COMPILE__)
-      asm volatile("" : "+a"(acc[j][i]));
-#endif
-    }
+    for (int i = 0; i < MB; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  pin(acc);
   mfma_guard();
 
   // Step j of a slice whose block 0 is `block` of the workgroup's, its
@@ -414,6 +410,7 @@ wgrad_pipe(PipeArgs p, TileMap map, int vec) {
     __builtin_amdgcn_s_waitcnt(0x0070);
   }
   mfma_guard();
+  pin(acc);  // (read after the guard only)
 
   typedef typename TypeOf<DT>::type Out;
   const int rows = p.F - (m0 + wm0), cols = p.N - (n0 + wn0);

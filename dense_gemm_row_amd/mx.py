@@ -27,8 +27,8 @@ BLOCK = 32     # values per scale
 
 FORMATS = {E2M1: 0, E4M3: 1}
 BLOCK_BYTES = {E2M1: 16, E4M3: 32}
-EXPORTS = ["gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx_matmul", "gemm_mx_wgrad",
-           "gemm_mx_wgrad_workspace_bytes"]
+EXPORTS = ["gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx_matmul", "gemm_mx_matmul_values",
+           "gemm_mx_matmul_values_workspace_bytes", "gemm_mx_wgrad", "gemm_mx_wgrad_workspace_bytes"]
 
 _declared = None
 
@@ -45,7 +45,12 @@ def lib():
                                      ctypes.POINTER(gemm.GemmEpilogue)]
         L.gemm_mx_wgrad.argtypes = [i32, i32, i64, i64, i64, p, i64, p, i64, p, i64, p, i64, f, f,
                                     p, i64, p]
-        for name in ("gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx_matmul", "gemm_mx_wgrad"):
+        L.gemm_mx_matmul_values.argtypes = [i32, i32, i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p,
+                                            ctypes.POINTER(gemm.GemmEpilogue)]
+        L.gemm_mx_matmul_values_workspace_bytes.argtypes = [i64, i64]
+        L.gemm_mx_matmul_values_workspace_bytes.restype = i64
+        for name in ("gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx_matmul", "gemm_mx_matmul_values",
+                     "gemm_mx_wgrad"):
             getattr(L, name).restype = ctypes.c_int
         L.gemm_mx_wgrad_workspace_bytes.argtypes = [i32, i64, i64, i64]
         L.gemm_mx_wgrad_workspace_bytes.restype = i64
@@ -67,6 +72,16 @@ def gemm_mx_matmul(c_dtype, M, N, K, A, lda, As, ldas, Bt, ldbt, Bs, ldbs, C, ld
                                 ctypes.byref(epi) if epi is not None else None)
 
 
+def gemm_mx_matmul_values(a_dtype, c_dtype, M, N, K, X, ldx, Bt, ldbt, Bs, ldbs, C, ldc, workspace=None,
+                          workspace_bytes=0, stream=None, epi: gemm.GemmEpilogue | None = None) -> int:
+    return lib().gemm_mx_matmul_values(a_dtype, c_dtype, M, N, K, X, ldx, Bt, ldbt, Bs, ldbs, C, ldc, workspace,
+                                       workspace_bytes, stream, ctypes.byref(epi) if epi is not None else None)
+
+
+def gemm_mx_matmul_values_workspace_bytes(M, K) -> int:
+    return lib().gemm_mx_matmul_values_workspace_bytes(M, K)
+
+
 def gemm_mx_wgrad(y_dtype, c_dtype, T, F, N, codes, ldq, scales, lds, dY, ldy, dW, ldw, alpha=1.0, beta=0.0,
                   workspace=None, workspace_bytes=0, stream=None) -> int:
     return lib().gemm_mx_wgrad(y_dtype, c_dtype, T, F, N, codes, ldq, scales, lds, dY, ldy, dW, ldw,
@@ -78,18 +93,24 @@ def gemm_mx_wgrad_workspace_bytes(y_dtype, T, F, N) -> int:
 
 
 # --------------------------------------------------------------------------
-# Torch forms.
+# Torch forms.  A small call takes about as long as the host needs to make it,
+# so these look at every tensor once and ask torch for little: the current
+# stream's handle without a Stream object, one allocation a result.
 # --------------------------------------------------------------------------
-_DTYPES = None
+_FAR = 1 << 26  # strides from here on, in bytes, take the workspace in gemm_mx_matmul_values
+_torch = None
+_DTYPES = {}       # torch dtype -> library dtype
+_raw_stream = None  # device index -> handle of torch's current stream
 
 
-def _dtypes():
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.float32: gemm.DTYPE_F32, torch.float16: gemm.DTYPE_F16,
-                   torch.bfloat16: gemm.DTYPE_BF16}
-    return _DTYPES
+def _load():
+    global _torch, _raw_stream
+    import torch
+    _DTYPES.update({torch.float32: gemm.DTYPE_F32, torch.float16: gemm.DTYPE_F16,
+                    torch.bfloat16: gemm.DTYPE_BF16})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
 
 
 class MxTensor:
@@ -103,13 +124,14 @@ class MxTensor:
         if fmt not in FORMATS:
             raise ValueError(f"unknown format {fmt!r}: {E2M1!r} or {E4M3!r}")
         blocks = -(-cols // BLOCK)
-        if codes.dim() != 2 or scales.dim() != 2 or codes.element_size() != 1 or scales.element_size() != 1:
+        cs, ss = codes.shape, scales.shape
+        if len(cs) != 2 or len(ss) != 2 or codes.element_size() != 1 or scales.element_size() != 1:
             raise ValueError("codes and scales must be 2-D tensors of bytes")
-        if codes.shape[0] != scales.shape[0]:
+        if cs[0] != ss[0]:
             raise ValueError("codes and scales differ in rows")
-        if codes.shape[1] != blocks * BLOCK_BYTES[fmt] or scales.shape[1] != blocks:
+        if cs[1] != blocks * BLOCK_BYTES[fmt] or ss[1] != blocks:
             raise ValueError(f"{cols} columns need {blocks * BLOCK_BYTES[fmt]} code bytes and {blocks} scales a row")
-        if (codes.shape[1] > 1 and codes.stride(1) != 1) or (scales.shape[1] > 1 and scales.stride(1) != 1):
+        if (cs[1] > 1 and codes.stride(1) != 1) or (blocks > 1 and scales.stride(1) != 1):
             raise ValueError("rows must be contiguous (unit column stride)")
         if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
@@ -132,48 +154,62 @@ class MxTensor:
 
     def _args(self):
         c, s = self.codes, self.scales
-        many = c.shape[0] > 1
-        return (c.data_ptr(), c.stride(0) if many else -(-c.shape[1] // 16) * 16,
-                s.data_ptr(), s.stride(0) if many else s.shape[1])
+        rows, width = c.shape
+        if rows > 1:
+            return c.data_ptr(), c.stride(0), s.data_ptr(), s.stride(0)
+        # A single row's stride means nothing: its length, in whole words.
+        return c.data_ptr(), -(-width // 16) * 16, s.data_ptr(), -(-s.shape[1] // 4) * 4
 
     def __repr__(self) -> str:
         return f"MxTensor({self.rows} x {self.cols}, {self.fmt}, {self.device})"
 
 
-def _stream(t, stream):
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+class _Launch:
+    """The launch stream of a call on `index`, and allocations on it, so that
+    torch's allocator orders their reuse after the kernels (the current stream
+    is left as it is)."""
+    __slots__ = ("handle", "other", "device")
 
+    def __init__(self, t, stream):
+        if _torch is None:
+            _load()
+        self.device = t.device
+        current = _raw_stream(t.get_device())
+        if stream is None:
+            self.handle, self.other = current, False
+        else:
+            self.handle = stream.cuda_stream if isinstance(stream, _torch.cuda.Stream) else int(stream)
+            self.other = self.handle != current
 
-class _On:
-    """Allocations on the launch stream, so that torch's allocator orders
-    their reuse after the kernels (the current stream is left as it is)."""
+    def empty(self, shape, dtype):
+        if not self.other:
+            return _torch.empty(shape, dtype=dtype, device=self.device)
+        with _torch.cuda.stream(_torch.cuda.ExternalStream(self.handle, device=self.device)):
+            return _torch.empty(shape, dtype=dtype, device=self.device)
 
-    def __init__(self, device, stream):
-        import torch
-        self.ctx = None
-        if stream != torch.cuda.current_stream(device).cuda_stream:
-            self.ctx = torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+    def coded(self, rows, cols, fmt):
+        if not self.other:
+            return empty(rows, cols, fmt, self.device)
+        with _torch.cuda.stream(_torch.cuda.ExternalStream(self.handle, device=self.device)):
+            return empty(rows, cols, fmt, self.device)
 
 
 def _dense(t, name):
+    """(library dtype, rows, columns, leading dimension) of a GPU matrix."""
+    if _torch is None:
+        _load()
     if t.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D tensor")
-    if t.dtype not in _dtypes():
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    return gemm._ld(t)
+    rows, cols = t.shape
+    sr, sc = t.stride()
+    if cols > 1 and sc != 1:
+        raise ValueError("rows must be contiguous (unit column stride)")
+    return dtype, rows, cols, max(sr if rows > 1 else cols, 1)
 
 
 def _coded(q, name, fmt):
@@ -195,61 +231,65 @@ def _check(st, name):
         raise gemm.GemmError(st, name)
 
 
+def _out_dtype(dtype, default, name):
+    dtype = dtype or default
+    if dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16")
+    return dtype
+
+
 def empty(rows: int, cols: int, fmt: str, device) -> MxTensor:
     """An uninitialised coded matrix; scale rows are a multiple of 4 bytes."""
-    import torch
+    if _torch is None:
+        _load()
     if fmt not in FORMATS:
         raise ValueError(f"unknown format {fmt!r}: {E2M1!r} or {E4M3!r}")
     blocks = -(-cols // BLOCK)
-    codes = torch.empty((rows, blocks * BLOCK_BYTES[fmt]), dtype=torch.uint8, device=device)
-    scales = torch.empty((rows, -(-blocks // 4) * 4), dtype=torch.uint8, device=device)
-    return MxTensor(codes, scales[:, :blocks], cols, fmt)
+    q = MxTensor.__new__(MxTensor)  # (as the checks of __init__ would have it)
+    q.codes = _torch.empty((rows, blocks * BLOCK_BYTES[fmt]), dtype=_torch.uint8, device=device)
+    if blocks % 4 == 0:
+        q.scales = _torch.empty((rows, blocks), dtype=_torch.uint8, device=device)
+    else:
+        q.scales = _torch.empty_strided((rows, blocks), (-(-blocks // 4) * 4, 1), dtype=_torch.uint8, device=device)
+    q.cols, q.fmt = cols, fmt
+    return q
 
 
 def quantize(x, fmt: str = E2M1, transposed: bool = False, out: MxTensor | None = None, stream=None) -> MxTensor:
     """The coded form of the 2-D tensor x (blocks along its rows), or with
     ``transposed`` of x.T (blocks down its columns)."""
-    ldx = _dense(x, "x")
-    rows, cols = x.shape
+    dtype, rows, cols, ldx = _dense(x, "x")
     shape = (cols, rows) if transposed else (rows, cols)
-    s = _stream(x, stream)
+    on = _Launch(x, stream)
     if out is None:
-        with _On(x.device, s):
-            out = empty(*shape, fmt, x.device)
+        out = on.coded(*shape, fmt)
     else:
         _coded(out, "out", fmt)
         _same_device(x, out)
         if out.shape != shape:
             raise ValueError(f"out has shape {out.shape}, not {shape}")
-    c, ldq, sc, lds = out._args()
-    _check(lib().gemm_mx_quantize(_dtypes()[x.dtype], FORMATS[fmt], int(transposed), rows, cols, x.data_ptr(), ldx,
-                                  c, ldq, sc, lds, s), "gemm_mx_quantize")
+    _check(lib().gemm_mx_quantize(dtype, FORMATS[fmt], 1 if transposed else 0, rows, cols, x.data_ptr(), ldx,
+                                  *out._args(), on.handle), "gemm_mx_quantize")
     return out
 
 
 def dequantize(q: MxTensor, dtype=None, transposed: bool = False, out=None, stream=None):
     """The values of a coded matrix (transposed: of its transpose) as a
     tensor of ``dtype`` (default bfloat16)."""
-    import torch
     if not isinstance(q, MxTensor):
         raise TypeError("q must be an MxTensor")
     if not q.codes.is_cuda:
         raise ValueError("q must be on the GPU")
-    shape = (q.cols, q.rows) if transposed else (q.rows, q.cols)
-    s = _stream(q, stream)
+    rows, cols = (q.cols, q.rows) if transposed else q.shape
+    on = _Launch(q.codes, stream)
     if out is None:
-        dtype = dtype or torch.bfloat16
-        if dtype not in _dtypes():
-            raise TypeError("dtype must be float32, float16 or bfloat16")
-        with _On(q.device, s):
-            out = torch.empty(shape, dtype=dtype, device=q.device)
-    elif tuple(out.shape) != shape or (dtype is not None and out.dtype != dtype):
+        out = on.empty((rows, cols), _out_dtype(dtype, _torch.bfloat16, "dtype"))
+    elif tuple(out.shape) != (rows, cols) or (dtype is not None and out.dtype != dtype):
         raise ValueError("out has the wrong shape or dtype")
-    ldx = _dense(out, "out")
+    x_dtype, _, _, ldx = _dense(out, "out")
     _same_device(q, out)
-    c, ldq, sc, lds = q._args()
-    _check(lib().gemm_mx_dequantize(_dtypes()[out.dtype], FORMATS[q.fmt], int(transposed), shape[0], shape[1],
-                                    c, ldq, sc, lds, out.data_ptr(), ldx, s), "gemm_mx_dequantize")
+    _check(lib().gemm_mx_dequantize(x_dtype, FORMATS[q.fmt], 1 if transposed else 0, rows, cols, *q._args(),
+                                    out.data_ptr(), ldx, on.handle), "gemm_mx_dequantize")
     return out
 
 
@@ -260,41 +300,46 @@ def matmul(a, b: MxTensor, out=None, out_dtype=None, alpha: float = 1.0, beta: f
     MxTensor (of a K x N weight: ``quantize(w, transposed=True)``).  The
     result is bfloat16 unless out or out_dtype says otherwise.  bias: N
     float32 values."""
-    import torch
     _coded(b, "b", E2M1)
-    if not isinstance(a, MxTensor):
-        _dense(a, "a")
+    values = not isinstance(a, MxTensor)
+    if values:
+        a_dtype, M, K, lda = _dense(a, "a")
     else:
         _coded(a, "a", E2M1)
+        M, K = a.shape
     _same_device(a, b)
-    M, K = a.shape
     N = b.rows
     if b.cols != K:
         raise ValueError(f"inner dimensions differ: {K} vs {b.cols}")
-    s = _stream(b, stream)
-    if not isinstance(a, MxTensor):
-        a = quantize(a, E2M1, stream=s)
+    on = _Launch(b.codes, stream)
     if out is None:
         if beta != 0.0:
             raise ValueError("beta needs out")
-        out_dtype = out_dtype or torch.bfloat16
-        if out_dtype not in _dtypes():
-            raise TypeError("out_dtype must be float32, float16 or bfloat16")
-        with _On(b.device, s):
-            out = torch.empty((M, N), dtype=out_dtype, device=b.device)
+        out = on.empty((M, N), _out_dtype(out_dtype, _torch.bfloat16, "out_dtype"))
     elif tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out has the wrong shape or dtype")
-    ldc = _dense(out, "out")
+    c_dtype, _, _, ldc = _dense(out, "out")
     _same_device(out, b)
     epi = None
     if alpha != 1.0 or beta != 0.0 or bias is not None or act != gemm.ACT_NONE:
-        if bias is not None and (bias.dtype != torch.float32 or bias.numel() != N or not bias.is_contiguous()
+        if bias is not None and (bias.dtype != _torch.float32 or bias.numel() != N or not bias.is_contiguous()
                                  or bias.device != b.device):
             raise ValueError("bias must be a contiguous float32 GPU tensor of N values")
         epi = ctypes.byref(gemm.GemmEpilogue(float(alpha), float(beta),
                                              bias.data_ptr() if bias is not None else None, int(act)))
-    _check(lib().gemm_mx_matmul(_dtypes()[out.dtype], M, N, K, *a._args(), *b._args(), out.data_ptr(), ldc, s, epi),
-           "gemm_mx_matmul")
+    if not values:
+        _check(lib().gemm_mx_matmul(c_dtype, M, N, K, *a._args(), *b._args(), out.data_ptr(), ldc, on.handle, epi),
+               "gemm_mx_matmul")
+        return out
+    x, coded, row = a.data_ptr(), b._args(), lda * a.element_size()
+    # A decoding step's few rows need no workspace (the header's conditions).
+    inside = (M <= 16 and (x | row) % 16 == 0 and (coded[2] | coded[3]) % 4 == 0 and N <= _FAR
+              and max(row, coded[1], coded[3]) < _FAR)
+    need = 0 if inside else lib().gemm_mx_matmul_values_workspace_bytes(M, K)
+    ws = on.empty(need, _torch.uint8) if need > 0 else None
+    _check(lib().gemm_mx_matmul_values(a_dtype, c_dtype, M, N, K, x, lda, *coded, out.data_ptr(), ldc,
+                                       ws.data_ptr() if ws is not None else None, need, on.handle, epi),
+           "gemm_mx_matmul_values")
     return out
 
 
@@ -315,36 +360,25 @@ def weight_grad(kept: MxTensor, dy, out=None, out_dtype=None, alpha: float = 1.0
     """dW = alpha * x.T @ dy + beta * out from x's checkpoint (features x
     tokens) and dy (tokens x N): features x N, float32 unless out or
     out_dtype says otherwise.  beta = 1 accumulates over micro-batches."""
-    import torch
     _coded(kept, "kept", E4M3)
-    ldy = _dense(dy, "dy")
+    y_dtype, rows, N, ldy = _dense(dy, "dy")
     _same_device(kept, dy)
     F, T = kept.shape
-    N = dy.shape[1]
-    if dy.shape[0] != T:
-        raise ValueError(f"tokens differ: {T} vs {dy.shape[0]}")
-    s = _stream(dy, stream)
-    y_dtype = _dtypes()[dy.dtype]
-    need = lib().gemm_mx_wgrad_workspace_bytes(y_dtype, T, F, N)
-    ws = None
-    if out is not None and (tuple(out.shape) != (F, N) or (out_dtype is not None and out.dtype != out_dtype)):
-        raise ValueError("out has the wrong shape or dtype")
+    if rows != T:
+        raise ValueError(f"tokens differ: {T} vs {rows}")
+    on = _Launch(dy, stream)
     if out is None:
         if beta != 0.0:
             raise ValueError("beta needs out")
-        out_dtype = out_dtype or torch.float32
-        if out_dtype not in _dtypes():
-            raise TypeError("out_dtype must be float32, float16 or bfloat16")
-    with _On(dy.device, s):
-        if out is None:
-            out = torch.empty((F, N), dtype=out_dtype, device=dy.device)
-        if need > 0:
-            ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
-    ldw = _dense(out, "out")
+        out = on.empty((F, N), _out_dtype(out_dtype, _torch.float32, "out_dtype"))
+    elif tuple(out.shape) != (F, N) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out has the wrong shape or dtype")
+    c_dtype, _, _, ldw = _dense(out, "out")
     _same_device(out, dy)
-    _check(lib().gemm_mx_wgrad(y_dtype, _dtypes()[out.dtype], T, F, N, *kept._args(), dy.data_ptr(), ldy,
-                               out.data_ptr(), ldw, float(alpha), float(beta),
-                               ws.data_ptr() if ws is not None else None, need if ws is not None else 0, s),
+    need = lib().gemm_mx_wgrad_workspace_bytes(y_dtype, T, F, N)
+    ws = on.empty(need, _torch.uint8) if need > 0 else None
+    _check(lib().gemm_mx_wgrad(y_dtype, c_dtype, T, F, N, *kept._args(), dy.data_ptr(), ldy, out.data_ptr(), ldw,
+                               alpha, beta, ws.data_ptr() if ws is not None else None, max(need, 0), on.handle),
            "gemm_mx_wgrad")
     return out
 

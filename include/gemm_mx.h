@@ -97,6 +97,25 @@ gemm_status_t gemm_mx_matmul(int32_t c_dtype, int64_t M, int64_t N, int64_t K,
                              void *C, int64_t ldc, void *stream, const gemm_epilogue_t *epi);
 
 /*
+ * The same product with A = X quantised to E2M1 on the way (X is M x K of
+ * type a_dtype: F32, F16, BF16): what gemm_mx_quantize and gemm_mx_matmul
+ * give one after the other.  Up to 16 rows, a decoding step's, are encoded
+ * inside the product, in one launch, if X's rows are 16-byte aligned, Bt's
+ * scale rows 4-byte aligned, every row stride below 2^26 bytes and N at most
+ * 2^26; `workspace` may be NULL then.  Otherwise the codes go through it
+ * (gemm_mx_matmul_values_workspace_bytes bytes, 16-byte aligned, not
+ * overlapping the operands; too small a one -> INVALID_ARG).
+ */
+gemm_status_t gemm_mx_matmul_values(int32_t a_dtype, int32_t c_dtype, int64_t M, int64_t N, int64_t K,
+                                    const void *X, int64_t ldx,
+                                    const uint8_t *Bt, int64_t ldbt, const uint8_t *Bs, int64_t ldbs,
+                                    void *C, int64_t ldc, void *workspace, int64_t workspace_bytes,
+                                    void *stream, const gemm_epilogue_t *epi);
+
+/* Bytes of that workspace; -1 for a size that gemm_mx_matmul_values refuses. */
+int64_t gemm_mx_matmul_values_workspace_bytes(int64_t M, int64_t K);
+
+/*
  * Weight gradient from an 8-bit activation checkpoint: dW = alpha * X^T x dY
  * + beta * dW.  The checkpoint is x (T tokens x F features) quantised with
  * GEMM_MX_E4M3 and trans = 1: codes F x T, blocks of 32 tokens of one
