@@ -78,8 +78,12 @@ gemm_status_t check_format(int dtype, int format) {
   return GEMM_OK;
 }
 
-// Scale rows of whole 4-byte words, as the pipelined product takes them.
-int64_t scale_row(int64_t cols) { return (blocks_of(cols) + 3) / 4 * 4; }
+// Scale rows of whole 4-byte words, as the pipelined product takes them, or
+// (long ones) of whole 16 bytes, as it likes them.
+int64_t scale_row(int64_t cols) {
+  const int64_t nb = blocks_of(cols), unit = nb < 16 ? 4 : 16;
+  return (nb + unit - 1) / unit * unit;
+}
 
 // What both products share: sizes, Bt, C and the epilogue.
 gemm_status_t check_product(int c_dtype, int64_t M, int64_t N, int64_t K, const uint8_t* Bt, int64_t ldbt, const uint8_t* Bs,

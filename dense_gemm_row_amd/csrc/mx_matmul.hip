@@ -294,71 +294,99 @@ hipError_t launch_skinny(const MatmulArgs& a, hipStream_t stream) {
 //  * Codes go from memory to LDS with 16-byte LDS-direct copies, chunk q of
 //    row r at position q ^ (r/2)%8 of its 128-byte row, so that the 16 rows
 //    of an operand read hit distinct banks.
-//  * Scales: 8 bytes per row and slice, copied as two 4-byte pieces, read a
-//    byte at a time straight into the instruction's scale operand (the four
-//    lanes of a row read the same word).  In the last slice the blocks past
-//    the matrix read zeros kept behind the scales instead, since a row's
-//    bytes past its blocks may be anything (255 would be NaN).
+//  * Scales go to LDS for two slices at a time, 16 bytes of a row (SC = 16:
+//    one copy a wave and operand; SC = 4, for scale rows that are only 4-byte
+//    aligned, four).  A slice's two steps take blocks 2q and 2q + 1 for lane
+//    group q, so that a lane's scales for both are one 16-bit read, and the
+//    instruction picks the byte.  Bytes past the matrix' blocks may be
+//    anything (255 would be NaN) and are cleared in the register.
+//    (8192^3: 273 us with 8 bytes a slice in 4-byte copies and a byte read
+//    for each step.)
 //  * A k step is MB x NB matrix instructions in a fixed order; the next
 //    step's operand reads and the copies of the slice after next are placed
 //    between them.  One barrier per slice, before its last step (whose
 //    operands are in registers by then).
-// The operands are range-checked by the descriptors' and lanes' offsets:
-// rows and blocks past the matrix load zeros.
-template <int BM_, int BN_, int WM_, int WN_>
+// The operands are range-checked by the lanes' offsets: rows and blocks past
+// the matrix load zeros.
+template <int BM_, int BN_, int WM_, int WN_, int SC_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, SC = SC_;
   static constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N;
   static constexpr int MB = WM / 16, NB = WN / 16, NMMA = MB * NB;
   static constexpr int ROW = 128, KB = 8;  // bytes and blocks per row and slice
   static constexpr int A_STAGE = BM * ROW, B_STAGE = BN * ROW;
   static constexpr int IA = A_STAGE / 1024 / NW, IB = B_STAGE / 1024 / NW;
-  static constexpr int SA = BM * KB / 256 / NW, SB = BN * KB / 256 / NW;
-  static constexpr int LPS = IA + IB + SA + SB;
-  static_assert(IA > 0 && IB > 0 && SA > 0 && SB > 0, "copies split over the waves");
+  // Scale copies of a wave, for two slices: rows of 16 bytes.
+  static constexpr int SROW = 16, SPI = 64 * SC / SROW;  // rows of one copy
+  __host__ __device__ static constexpr int scale_copies(int rows) { return (rows + SPI * NW - 1) / (SPI * NW); }
+  static constexpr int SA = scale_copies(BM), SB = scale_copies(BN);
+  static constexpr int SA_STAGE = SA * SPI * NW * SROW, SB_STAGE = SB * SPI * NW * SROW;
+  static_assert(IA > 0 && IB > 0 && NW % 2 == 0, "copies split over the waves; 8 NW rows on, the chunk XOR repeats");
+  static_assert(SC == 4 || SC == 16, "scale pieces");
   __host__ __device__ static constexpr int byte(int r, int q) { return swz_off(r, q, ROW); }
-  // Scales of fragment f: 16 rows on.
-  static constexpr int SF = 16 * KB;
-  static constexpr int SA_STAGE = BM * KB + MB * SF, SB_STAGE = BN * KB + NB * SF;
-  // Slots among a step's NMMA instructions: operand f (A's, then B's), copy c.
-  __host__ __device__ static constexpr int rd_slot(int f) { return f * NMMA / (MB + NB); }
-  __host__ __device__ static constexpr int cp_slot(int c) { return c * NMMA / LPS; }
+  // Slots among a step's NMMA instructions: operand f (A's, then B's); its
+  // scales and their clearing, at least 6 instructions later and as many
+  // before the next step; copy c of n.
+  static constexpr int F = MB + NB;
+  struct Read {
+    __host__ __device__ static constexpr int at(int f) { return f * NMMA / F; }
+  };
+  struct Scale {
+    __host__ __device__ static constexpr int at(int f) { return f * NMMA / (2 * F); }
+  };
+  struct Clear {
+    __host__ __device__ static constexpr int at(int f) { return Scale::at(f) + 3 * NMMA / 8; }
+  };
+  template <int N>
+  struct Copy {
+    __host__ __device__ static constexpr int at(int c) { return c * NMMA / N; }
+  };
 };
 
+// A lane's offsets in the copies of a slice (codes) and of two (scales).
 template <class S>
 struct Copies {
   unsigned a[S::IA], b[S::IB], as[S::SA], bs[S::SB];
+  int q, sw;  // its chunk of a row; its first scale block of 16
 };
 
-// Copy C of a slice, whose descriptors start at it; `left` blocks of the
-// matrix are from its first on (<= 0: there is no such slice).
+// Copy C of a slice's codes (A's, then B's), whose descriptors start at it;
+// `left` blocks of the matrix are from its first on (<= 0: no such slice).
 template <class S, int C>
-__device__ __forceinline__ void copy_one(const uint8_t* Ab, const uint8_t* Bb, const uint8_t* As, const uint8_t* Bs,
-                                         const Copies<S>& o, int64_t slice, int left, uint8_t* la,
-                                         uint8_t* lb, uint8_t* lsa, uint8_t* lsb, int wave, int qa, int qb, int sw) {
+__device__ __forceinline__ void copy_codes(const uint8_t* A, const uint8_t* B, const Copies<S>& o, int64_t slice, int left,
+                                           uint8_t* la, uint8_t* lb, int wave) {
   // (Device pass only: the host pass does not know the descriptor type.)
 #if defined(__HIP_DEVICE_COMPILE__)
   const int range = left > 0 ? 0x7fffffff : 0;
   if constexpr (C < S::IA) {
-    constexpr int i = C;
-    const unsigned off = qa < left ? o.a[i] : OOB;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(Ab + slice * S::ROW, range),
-                                             (lds_void*)(la + 1024 * (i * S::NW + wave)), 16, off, 0, 0, 0);
-  } else if constexpr (C < S::IA + S::IB) {
-    constexpr int i = C - S::IA;
-    const unsigned off = qb < left ? o.b[i] : OOB;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(Bb + slice * S::ROW, range),
-                                             (lds_void*)(lb + 1024 * (i * S::NW + wave)), 16, off, 0, 0, 0);
-  } else if constexpr (C < S::IA + S::IB + S::SA) {
-    constexpr int i = C - S::IA - S::IB;
-    const unsigned off = sw < left ? o.as[i] : OOB;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(As + slice * S::KB, range),
-                                             (lds_void*)(lsa + 256 * (i * S::NW + wave)), 4, off, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(A + slice * S::ROW, range),
+                                             (lds_void*)(la + 1024 * (C * S::NW + wave)), 16, o.q < left ? o.a[C] : OOB, 0,
+                                             0, 0);
   } else {
-    constexpr int i = C - S::IA - S::IB - S::SA;
-    const unsigned off = sw < left ? o.bs[i] : OOB;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(Bs + slice * S::KB, range),
-                                             (lds_void*)(lsb + 256 * (i * S::NW + wave)), 4, off, 0, 0, 0);
+    constexpr int i = C - S::IA;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(B + slice * S::ROW, range),
+                                             (lds_void*)(lb + 1024 * (i * S::NW + wave)), 16, o.q < left ? o.b[i] : OOB, 0,
+                                             0, 0);
+  }
+#endif
+}
+
+// The same of the scales of a pair of slices.
+template <class S, int C>
+__device__ __forceinline__ void copy_scales(const uint8_t* A, const uint8_t* B, const Copies<S>& o, int64_t pair, int left,
+                                            uint8_t* la, uint8_t* lb, int wave) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int range = left > 0 ? 0x7fffffff : 0;
+  constexpr int BYTES = S::SPI * S::SROW;  // of one copy
+  if constexpr (C < S::SA) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(A + pair * S::SROW, range),
+                                             (lds_void*)(la + BYTES * (C * S::NW + wave)), S::SC,
+                                             o.sw < left ? o.as[C] : OOB, 0, 0, 0);
+  } else {
+    constexpr int i = C - S::SA;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(B + pair * S::SROW, range),
+                                             (lds_void*)(lb + BYTES * (i * S::NW + wave)), S::SC,
+                                             o.sw < left ? o.bs[i] : OOB, 0, 0, 0);
   }
 #endif
 }
@@ -366,7 +394,7 @@ __device__ __forceinline__ void copy_one(const uint8_t* Ab, const uint8_t* Bb, c
 template <int DT, class S, bool EPI>
 __global__ void __launch_bounds__(64 * S::NW)
 matmul_pipe(MatmulArgs p, TileMap map, int vec) {
-  constexpr int MB = S::MB, NB = S::NB;
+  constexpr int MB = S::MB, NB = S::NB, F = S::F, NC = S::IA + S::IB, NSC = S::SA + S::SB;
   __shared__ __attribute__((aligned(1024))) uint8_t a0[S::A_STAGE], b0[S::B_STAGE], a1[S::A_STAGE], b1[S::B_STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[S::SA_STAGE], sb0[S::SB_STAGE], sa1[S::SA_STAGE], sb1[S::SB_STAGE];
   int tm, tn;
@@ -382,47 +410,42 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
   const uint8_t* Bb = p.b.codes + (int64_t)n0 * p.b.ldq;
   const uint8_t* As = p.a.scales + (int64_t)m0 * p.a.lds;
   const uint8_t* Bs = p.b.scales + (int64_t)n0 * p.b.lds;
-  // This lane's place in the copies: 8 rows of 8 chunks, 32 rows of two
-  // scale words; a chunk's index is the same for all copies of an operand.
+  // A code copy is 8 rows of 8 chunks, the chunk index the same for all of a
+  // wave's; a scale copy SPI rows of 16 bytes.
   Copies<S> o;
-  const int qa = (l % 8) ^ swz_row(8 * wave + l / 8, S::ROW), qb = qa;
-  static_assert(S::NW % 2 == 0, "8 NW rows on, the chunk XOR repeats");
-  const int sw = 4 * (l % 2);
+  o.q = (l % 8) ^ swz_row(8 * wave + l / 8, S::ROW);
+  o.sw = S::SC == 4 ? 4 * (l % 4) : 0;
 #pragma unroll
   for (int i = 0; i < S::IA; ++i) {
     const int row = 8 * (i * S::NW + wave) + l / 8;
-    o.a[i] = m0 + row < p.M ? (unsigned)(row * (int)p.a.ldq + 16 * qa) : OOB;
+    o.a[i] = m0 + row < p.M ? (unsigned)(row * (int)p.a.ldq + 16 * o.q) : OOB;
   }
 #pragma unroll
   for (int i = 0; i < S::IB; ++i) {
     const int row = 8 * (i * S::NW + wave) + l / 8;
-    o.b[i] = n0 + row < p.N ? (unsigned)(row * (int)p.b.ldq + 16 * qb) : OOB;
+    o.b[i] = n0 + row < p.N ? (unsigned)(row * (int)p.b.ldq + 16 * o.q) : OOB;
   }
 #pragma unroll
   for (int i = 0; i < S::SA; ++i) {
-    const int row = 32 * (i * S::NW + wave) + l / 2;
-    o.as[i] = m0 + row < p.M ? (unsigned)(row * (int)p.a.lds + sw) : OOB;
+    const int row = S::SPI * (i * S::NW + wave) + l / (S::SROW / S::SC);
+    o.as[i] = row < S::BM && m0 + row < p.M ? (unsigned)(row * (int)p.a.lds + o.sw) : OOB;
   }
 #pragma unroll
   for (int i = 0; i < S::SB; ++i) {
-    const int row = 32 * (i * S::NW + wave) + l / 2;
-    o.bs[i] = n0 + row < p.N ? (unsigned)(row * (int)p.b.lds + sw) : OOB;
+    const int row = S::SPI * (i * S::NW + wave) + l / (S::SROW / S::SC);
+    o.bs[i] = row < S::BN && n0 + row < p.N ? (unsigned)(row * (int)p.b.lds + o.sw) : OOB;
   }
-  for (int i = tid; i < MB * S::SF / 4; i += 64 * S::NW)
-    reinterpret_cast<unsigned*>(sa0 + S::BM * S::KB)[i] = reinterpret_cast<unsigned*>(sa1 + S::BM * S::KB)[i] = 0u;
-  for (int i = tid; i < NB * S::SF / 4; i += 64 * S::NW)
-    reinterpret_cast<unsigned*>(sb0 + S::BN * S::KB)[i] = reinterpret_cast<unsigned*>(sb1 + S::BN * S::KB)[i] = 0u;
   // Operand reads: byte offsets of the two steps' first fragments.
   int a_fb[2], b_fb[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    a_fb[j] = S::byte(wm0 + r, 4 * j + q);
-    b_fb[j] = S::byte(wn0 + r, 4 * j + q);
+    a_fb[j] = S::byte(wm0 + r, 2 * q + j);
+    b_fb[j] = S::byte(wn0 + r, 2 * q + j);
   }
-  const int sa_fb = (wm0 + r) * S::KB + q, sb_fb = (wn0 + r) * S::KB + q;
+  const int sa_fb = (wm0 + r) * S::SROW + 2 * q, sb_fb = (wn0 + r) * S::SROW + 2 * q;
 
-  i32x4 fa[2][MB], fb[2][NB];
-  int ga[2][MB], gb[2][NB];
+  i32x4 fa[2][MB], fb[2][NB];  // by step
+  int ga[2][MB], gb[2][NB];    // by slice
   f32x4 acc[NB][MB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
@@ -431,64 +454,114 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
   pin(acc);
   mfma_guard();
 
-  // Operand f of step j of slice t into register set `buf`.
-  auto read_op = [&](int buf, const uint8_t* la, const uint8_t* lb, const uint8_t* lsa, const uint8_t* lsb, int j, int t,
-                     auto F) __attribute__((always_inline)) {
-    constexpr int f = decltype(F)::value;
-    const bool live = S::KB * t + 4 * j + q < nb;
-    if constexpr (f < MB) {
-      fa[buf][f] = *(const lds_i32x4*)(la + a_fb[j] + f * 16 * S::ROW);
-      ga[buf][f] = *(const lds_u8*)(lsa + (live ? sa_fb + 4 * j : S::BM * S::KB) + f * S::SF);
-    } else {
-      constexpr int g = f - MB;
-      fb[buf][g] = *(const lds_i32x4*)(lb + b_fb[j] + g * 16 * S::ROW);
-      gb[buf][g] = *(const lds_u8*)(lsb + (live ? sb_fb + 4 * j : S::BN * S::KB) + g * S::SF);
-    }
+  // Operand f of step j from a stage.
+  auto read_op = [&](const uint8_t* la, const uint8_t* lb, auto J, auto F_) __attribute__((always_inline)) {
+    constexpr int j = decltype(J)::value, f = decltype(F_)::value;
+    if constexpr (f < MB)
+      fa[j][f] = *(const lds_i32x4*)(la + a_fb[j] + f * 16 * S::ROW);
+    else
+      fb[j][f - MB] = *(const lds_i32x4*)(lb + b_fb[j] + (f - MB) * 16 * S::ROW);
   };
-  auto step = [&](int cur, auto&& rd, auto&& cp) __attribute__((always_inline)) {
+  // Its scales in slice c of a pair, and their clearing: `mask` has the
+  // bytes of blocks inside the matrix.
+  auto read_scale = [&](const uint8_t* lsa, const uint8_t* lsb, auto C_, auto F_) __attribute__((always_inline)) {
+    constexpr int c = decltype(C_)::value, f = decltype(F_)::value;
+    if constexpr (f < MB)
+      ga[c][f] = *(const lds_u16*)(lsa + sa_fb + 8 * c + f * 16 * S::SROW);
+    else
+      gb[c][f - MB] = *(const lds_u16*)(lsb + sb_fb + 8 * c + (f - MB) * 16 * S::SROW);
+  };
+  auto clear_scale = [&](int mask, auto C_, auto F_) __attribute__((always_inline)) {
+    constexpr int c = decltype(C_)::value, f = decltype(F_)::value;
+    if constexpr (f < MB) ga[c][f] &= mask;
+    else gb[c][f - MB] &= mask;
+  };
+  auto mask_of = [&](int t) __attribute__((always_inline)) {
+    const int first = S::KB * t + 2 * q;
+    return first + 1 < nb ? 0xffff : first < nb ? 0xff : 0;
+  };
+  // Step j of a slice c; `between` runs after each instruction.
+  auto step = [&](auto J, auto C_, auto&& between) __attribute__((always_inline)) {
     static_for([&](auto I) __attribute__((always_inline)) {
-      constexpr int i = decltype(I)::value;
-      mfma_fp4_asm(acc[i / MB][i % MB], fb[cur][i / MB], fa[cur][i % MB], gb[cur][i / MB], ga[cur][i % MB]);
-      static_for([&](auto F) __attribute__((always_inline)) {
-        if constexpr (S::rd_slot(decltype(F)::value) == i) rd(F);
-      }, std::make_integer_sequence<int, MB + NB>{});
-      static_for([&](auto C) __attribute__((always_inline)) {
-        if constexpr (S::cp_slot(decltype(C)::value) == i) cp(C);
-      }, std::make_integer_sequence<int, S::LPS>{});
+      constexpr int i = decltype(I)::value, j = decltype(J)::value, c = decltype(C_)::value;
+      mfma_fp4_asm<j>(acc[i / MB][i % MB], fb[j][i / MB], fa[j][i % MB], gb[c][i / MB], ga[c][i % MB]);
+      between(I);
       __builtin_amdgcn_sched_barrier(0);
     }, std::make_integer_sequence<int, S::NMMA>{});
   };
-  // Slice t from stage 0 or 1.
-  auto slice = [&](int t, auto C_) __attribute__((always_inline)) {
-    constexpr int c = decltype(C_)::value;
-    uint8_t *la = c ? a1 : a0, *lb = c ? b1 : b0, *lsa = c ? sa1 : sa0, *lsb = c ? sb1 : sb0;
-    uint8_t *na = c ? a0 : a1, *nbp = c ? b0 : b1, *nsa = c ? sa0 : sa1, *nsb = c ? sb0 : sb1;
-    step(0, [&](auto F) __attribute__((always_inline)) { read_op(1, la, lb, lsa, lsb, 1, t, F); }, [](auto) {});
+  auto at_slot = [&](auto I, auto SLOT, auto N, auto&& f) __attribute__((always_inline)) {
+    static_for([&](auto X) __attribute__((always_inline)) {
+      if constexpr (decltype(SLOT)::at(decltype(X)::value) == decltype(I)::value) f(X);
+    }, std::make_integer_sequence<int, decltype(N)::value>{});
+  };
+  // Slice t: number c of its pair, whose scales are in buffer PAR.
+  auto slice = [&](int t, auto C_, auto PAR) __attribute__((always_inline)) {
+    constexpr int c = decltype(C_)::value, par = decltype(PAR)::value;
+    uint8_t *la = c ? a1 : a0, *lb = c ? b1 : b0, *na = c ? a0 : a1, *nbp = c ? b0 : b1;
+    // The next slice's scales: this pair's, or the next one's.
+    constexpr int np = c ? 1 - par : par;
+    uint8_t *nsa = np ? sa1 : sa0, *nsb = np ? sb1 : sb0;
+    uint8_t *psa = par ? sa0 : sa1, *psb = par ? sb0 : sb1;  // the next pair's
+    step(IC<0>{}, IC<c>{}, [&](auto I) __attribute__((always_inline)) {
+      at_slot(I, typename S::Read{}, IC<F>{},
+              [&](auto X) __attribute__((always_inline)) { read_op(la, lb, IC<1>{}, X); });
+    });
     loop_barrier();  // slice t + 1 landed, stage c read by every wave
     __builtin_amdgcn_sched_barrier(0);
-    step(1, [&](auto F) __attribute__((always_inline)) { read_op(0, na, nbp, nsa, nsb, 0, t + 1, F); },
-         [&](auto Q) __attribute__((always_inline)) {
-           copy_one<S, decltype(Q)::value>(Ab, Bb, As, Bs, o, t + 2, nb - S::KB * (t + 2), la, lb, lsa, lsb, wave, qa,
-                                           qb, sw);
-         });
+    const int mask = mask_of(t + 1);
+    constexpr int n = c ? NC : NC + NSC;
+    step(IC<1>{}, IC<c>{}, [&](auto I) __attribute__((always_inline)) {
+      at_slot(I, typename S::Scale{}, IC<F>{},
+              [&](auto X) __attribute__((always_inline)) { read_scale(nsa, nsb, IC<1 - c>{}, X); });
+      at_slot(I, typename S::Read{}, IC<F>{},
+              [&](auto X) __attribute__((always_inline)) { read_op(na, nbp, IC<0>{}, X); });
+      at_slot(I, typename S::Clear{}, IC<F>{},
+              [&](auto X) __attribute__((always_inline)) { clear_scale(mask, IC<1 - c>{}, X); });
+      at_slot(I, typename S::template Copy<n>{}, IC<n>{}, [&](auto X) __attribute__((always_inline)) {
+        constexpr int x = decltype(X)::value;
+        if constexpr (x < NC)
+          copy_codes<S, x>(Ab, Bb, o, t + 2, nb - S::KB * (t + 2), la, lb, wave);
+        else
+          copy_scales<S, x - NC>(As, Bs, o, t / 2 + 1, nb - S::KB * (t + 2), psa, psb, wave);
+      });
+    });
+  };
+  auto copy_slice = [&](int t, uint8_t* la, uint8_t* lb) __attribute__((always_inline)) {
+    static_for([&](auto X) __attribute__((always_inline)) {
+      copy_codes<S, decltype(X)::value>(Ab, Bb, o, t, nb - S::KB * t, la, lb, wave);
+    }, std::make_integer_sequence<int, NC>{});
   };
   if (T > 0) {
-    static_for([&](auto Q) __attribute__((always_inline)) {
-      copy_one<S, decltype(Q)::value>(Ab, Bb, As, Bs, o, 0, nb, a0, b0, sa0, sb0, wave, qa, qb, sw);
-    }, std::make_integer_sequence<int, S::LPS>{});
-    static_for([&](auto Q) __attribute__((always_inline)) {
-      copy_one<S, decltype(Q)::value>(Ab, Bb, As, Bs, o, 1, nb - S::KB, a1, b1, sa1, sb1, wave, qa, qb, sw);
-    }, std::make_integer_sequence<int, S::LPS>{});
+    copy_slice(0, a0, b0);
+    static_for([&](auto X) __attribute__((always_inline)) {
+      copy_scales<S, decltype(X)::value>(As, Bs, o, 0, nb, sa0, sb0, wave);
+    }, std::make_integer_sequence<int, NSC>{});
+    copy_slice(1, a1, b1);
     loop_barrier();
-    static_for([&](auto F) __attribute__((always_inline)) { read_op(0, a0, b0, sa0, sb0, 0, 0, F); },
-               std::make_integer_sequence<int, MB + NB>{});
+    static_for([&](auto X) __attribute__((always_inline)) {
+      read_op(a0, b0, IC<0>{}, X);
+      read_scale(sa0, sb0, IC<0>{}, X);
+    }, std::make_integer_sequence<int, F>{});
+    static_for([&](auto X) __attribute__((always_inline)) { clear_scale(mask_of(0), IC<0>{}, X); },
+               std::make_integer_sequence<int, F>{});
+    mfma_guard();
     int t = 0;
-    for (; t + 2 <= T; t += 2) {
-      slice(t, IC<0>{});
-      slice(t + 1, IC<1>{});
+    for (; t + 4 <= T; t += 4) {
+      slice(t, IC<0>{}, IC<0>{});
+      slice(t + 1, IC<1>{}, IC<0>{});
+      slice(t + 2, IC<0>{}, IC<1>{});
+      slice(t + 3, IC<1>{}, IC<1>{});
     }
     mfma_guard();
-    if (t < T) slice(t, IC<0>{});
+    if (t < T) {
+      slice(t, IC<0>{}, IC<0>{});
+      mfma_guard();
+    }
+    if (t + 1 < T) {
+      slice(t + 1, IC<1>{}, IC<0>{});
+      mfma_guard();
+    }
+    if (t + 2 < T) slice(t + 2, IC<0>{}, IC<1>{});
     __builtin_amdgcn_s_waitcnt(0x0070);
   }
   mfma_guard();
@@ -529,7 +602,7 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
 }
 
 template <int DT, class S>
-hipError_t launch_pipe(const MatmulArgs& a, hipStream_t stream) {
+hipError_t launch_pipe_tile(const MatmulArgs& a, hipStream_t stream) {
   TileMap map{(a.M + S::BM - 1) / S::BM, (a.N + S::BN - 1) / S::BN, GEMM_ORDER_XCD, 4, kXcds};
   const int es = DT == GEMM_DTYPE_F32 ? 4 : 2;
   const int vec = ((uintptr_t)a.C % 16 == 0 && a.ldc * es % 16 == 0 && a.N * es % 16 == 0) ? 1 : 0;
@@ -539,6 +612,13 @@ hipError_t launch_pipe(const MatmulArgs& a, hipStream_t stream) {
   else
     hipLaunchKernelGGL((matmul_pipe<DT, S, false>), grid, block, 0, stream, a, map, vec);
   return hipGetLastError();
+}
+
+template <int DT, int BM, int BN, int WM, int WN>
+hipError_t launch_pipe(const MatmulArgs& a, hipStream_t stream) {
+  const bool wide = (((uintptr_t)a.a.scales | (uintptr_t)a.b.scales) % 16 | (a.a.lds | a.b.lds) % 16) == 0;
+  return wide ? launch_pipe_tile<DT, Tile<BM, BN, WM, WN, 16>>(a, stream)
+              : launch_pipe_tile<DT, Tile<BM, BN, WM, WN, 4>>(a, stream);
 }
 
 // What the pipelined kernel takes: scales in 4-byte words, a tile's rows
@@ -560,8 +640,8 @@ hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
   // fill the 256 CUs with a quarter of the outputs (4096^3: 39 against
   // 50 us; 2048^3: 19 against 10 us).
   const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (tiles >= 192) return launch_pipe<DT, Tile<256, 256, 128, 128>>(a, stream);
-  return launch_pipe<DT, Tile<128, 128, 64, 64>>(a, stream);
+  if (tiles >= 192) return launch_pipe<DT, 256, 256, 128, 128>(a, stream);
+  return launch_pipe<DT, 128, 128, 64, 64>(a, stream);
 }
 
 }  // namespace

@@ -23,6 +23,7 @@ typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
+typedef __attribute__((address_space(3))) unsigned short lds_u16;
 
 constexpr unsigned OOB = 0x80000000u;  // offset past every descriptor's range
 
@@ -57,10 +58,16 @@ __device__ __forceinline__ void loop_barrier() {
 // writers of an operand at least 4 wait states before its reader (operands
 // come from LDS reads, or are decoded several instructions ahead), and
 // touch the accumulators only outside a guard.
+// (BYTE: the byte of both scale operands that counts.)
+template <int BYTE>
 __device__ __forceinline__ void mfma_fp4_asm(f32x4& c, i32x4 a, i32x4 b, int sa, int sb) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-               : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+  if constexpr (BYTE == 0)
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                 : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+  else
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                 : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb));
 #endif
 }
 __device__ __forceinline__ void mfma_bf16_asm(f32x4& c, i32x4 a, i32x4 b) {

@@ -239,7 +239,8 @@ def _out_dtype(dtype, default, name):
 
 
 def empty(rows: int, cols: int, fmt: str, device) -> MxTensor:
-    """An uninitialised coded matrix; scale rows are a multiple of 4 bytes."""
+    """An uninitialised coded matrix; scale rows are a multiple of 4 bytes, or
+    of 16 where they are that long (the widest pieces the kernels copy)."""
     if _torch is None:
         _load()
     if fmt not in FORMATS:
@@ -247,10 +248,11 @@ def empty(rows: int, cols: int, fmt: str, device) -> MxTensor:
     blocks = -(-cols // BLOCK)
     q = MxTensor.__new__(MxTensor)  # (as the checks of __init__ would have it)
     q.codes = _torch.empty((rows, blocks * BLOCK_BYTES[fmt]), dtype=_torch.uint8, device=device)
-    if blocks % 4 == 0:
+    unit = 4 if blocks < 16 else 16
+    if blocks % unit == 0:
         q.scales = _torch.empty((rows, blocks), dtype=_torch.uint8, device=device)
     else:
-        q.scales = _torch.empty_strided((rows, blocks), (-(-blocks // 4) * 4, 1), dtype=_torch.uint8, device=device)
+        q.scales = _torch.empty_strided((rows, blocks), (-(-blocks // unit) * unit, 1), dtype=_torch.uint8, device=device)
     q.cols, q.fmt = cols, fmt
     return q
 
