@@ -291,15 +291,18 @@ hipError_t launch_skinny(const MatmulArgs& a, hipStream_t stream) {
 // The pipelined kernel: a workgroup of four waves computes BM x BN, each
 // wave WM x WN in 16 x 16 blocks, 256 k (128 bytes a row) per slice through
 // two LDS stages.
-//  * Codes go from memory to LDS with 16-byte LDS-direct copies, chunk q of
-//    row r at position q ^ (r/2)%8 of its 128-byte row, so that the 16 rows
-//    of an operand read hit distinct banks.
+//  * Codes go from memory to LDS with 16-byte LDS-direct copies.  A 16-byte
+//    read serves 16 lanes at a time, rows 0-3 and 12-15 of an even lane group
+//    with rows 4-11 of the next (or the other way round); with step j's chunk
+//    of group q at position (4j + q) ^ (r/2)%8 of row r's 128 bytes, those
+//    hit distinct banks.
 //  * Scales go to LDS for two slices at a time, 16 bytes of a row (SC = 16:
 //    one copy a wave and operand; SC = 4, for scale rows that are only 4-byte
 //    aligned, four).  A slice's two steps take blocks 2q and 2q + 1 for lane
-//    group q, so that a lane's scales for both are one 16-bit read, and the
-//    instruction picks the byte.  Bytes past the matrix' blocks may be
-//    anything (255 would be NaN) and are cleared in the register.
+//    group q, so that a lane's scales for both come with one read (of the
+//    word that two groups share), and the instruction picks the byte.  A
+//    bit-field extraction takes them out of the word and clears those past
+//    the matrix' blocks, which may be anything (255 would be NaN).
 //    (8192^3: 273 us with 8 bytes a slice in 4-byte copies and a byte read
 //    for each step.)
 //  * A k step is MB x NB matrix instructions in a fixed order; the next
@@ -323,9 +326,11 @@ struct Tile {
   static constexpr int SA_STAGE = SA * SPI * NW * SROW, SB_STAGE = SB * SPI * NW * SROW;
   static_assert(IA > 0 && IB > 0 && NW % 2 == 0, "copies split over the waves; 8 NW rows on, the chunk XOR repeats");
   static_assert(SC == 4 || SC == 16, "scale pieces");
-  __host__ __device__ static constexpr int byte(int r, int q) { return swz_off(r, q, ROW); }
+  // Position `slot` of a row, XORed by the row; the chunk that belongs there.
+  __host__ __device__ static constexpr int byte(int r, int slot) { return swz_off(r, slot, ROW); }
+  __host__ __device__ static constexpr int chunk_at(int slot) { return 2 * (slot % 4) + slot / 4; }
   // Slots among a step's NMMA instructions: operand f (A's, then B's); its
-  // scales and their clearing, at least 6 instructions later and as many
+  // scales and their extraction, at least 6 instructions later and as many
   // before the next step; copy c of n.
   static constexpr int F = MB + NB;
   struct Read {
@@ -334,7 +339,7 @@ struct Tile {
   struct Scale {
     __host__ __device__ static constexpr int at(int f) { return f * NMMA / (2 * F); }
   };
-  struct Clear {
+  struct Take {
     __host__ __device__ static constexpr int at(int f) { return Scale::at(f) + 3 * NMMA / 8; }
   };
   template <int N>
@@ -413,7 +418,7 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
   // A code copy is 8 rows of 8 chunks, the chunk index the same for all of a
   // wave's; a scale copy SPI rows of 16 bytes.
   Copies<S> o;
-  o.q = (l % 8) ^ swz_row(8 * wave + l / 8, S::ROW);
+  o.q = S::chunk_at((l % 8) ^ swz_row(8 * wave + l / 8, S::ROW));
   o.sw = S::SC == 4 ? 4 * (l % 4) : 0;
 #pragma unroll
   for (int i = 0; i < S::IA; ++i) {
@@ -439,10 +444,10 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
   int a_fb[2], b_fb[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    a_fb[j] = S::byte(wm0 + r, 2 * q + j);
-    b_fb[j] = S::byte(wn0 + r, 2 * q + j);
+    a_fb[j] = S::byte(wm0 + r, 4 * j + q);
+    b_fb[j] = S::byte(wn0 + r, 4 * j + q);
   }
-  const int sa_fb = (wm0 + r) * S::SROW + 2 * q, sb_fb = (wn0 + r) * S::SROW + 2 * q;
+  const int sa_fb = (wm0 + r) * S::SROW + q / 2 * 4, sb_fb = (wn0 + r) * S::SROW + q / 2 * 4;
 
   i32x4 fa[2][MB], fb[2][NB];  // by step
   int ga[2][MB], gb[2][NB];    // by slice
@@ -462,23 +467,26 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
     else
       fb[j][f - MB] = *(const lds_i32x4*)(lb + b_fb[j] + (f - MB) * 16 * S::ROW);
   };
-  // Its scales in slice c of a pair, and their clearing: `mask` has the
-  // bytes of blocks inside the matrix.
+  // Its scales in slice c of a pair, and their extraction: `bits` of them
+  // belong to blocks inside the matrix.
   auto read_scale = [&](const uint8_t* lsa, const uint8_t* lsb, auto C_, auto F_) __attribute__((always_inline)) {
     constexpr int c = decltype(C_)::value, f = decltype(F_)::value;
     if constexpr (f < MB)
-      ga[c][f] = *(const lds_u16*)(lsa + sa_fb + 8 * c + f * 16 * S::SROW);
+      ga[c][f] = (int)*(const lds_u32*)(lsa + sa_fb + 8 * c + f * 16 * S::SROW);
     else
-      gb[c][f - MB] = *(const lds_u16*)(lsb + sb_fb + 8 * c + (f - MB) * 16 * S::SROW);
+      gb[c][f - MB] = (int)*(const lds_u32*)(lsb + sb_fb + 8 * c + (f - MB) * 16 * S::SROW);
   };
-  auto clear_scale = [&](int mask, auto C_, auto F_) __attribute__((always_inline)) {
+  const int from = 16 * (q % 2);
+  auto take_scale = [&](int bits, auto C_, auto F_) __attribute__((always_inline)) {
     constexpr int c = decltype(C_)::value, f = decltype(F_)::value;
-    if constexpr (f < MB) ga[c][f] &= mask;
-    else gb[c][f - MB] &= mask;
+    if constexpr (f < MB)
+      ga[c][f] = (int)__builtin_amdgcn_ubfe((unsigned)ga[c][f], from, bits);
+    else
+      gb[c][f - MB] = (int)__builtin_amdgcn_ubfe((unsigned)gb[c][f - MB], from, bits);
   };
-  auto mask_of = [&](int t) __attribute__((always_inline)) {
+  auto bits_of = [&](int t) __attribute__((always_inline)) {
     const int first = S::KB * t + 2 * q;
-    return first + 1 < nb ? 0xffff : first < nb ? 0xff : 0;
+    return first + 1 < nb ? 16 : first < nb ? 8 : 0;
   };
   // Step j of a slice c; `between` runs after each instruction.
   auto step = [&](auto J, auto C_, auto&& between) __attribute__((always_inline)) {
@@ -508,15 +516,15 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
     });
     loop_barrier();  // slice t + 1 landed, stage c read by every wave
     __builtin_amdgcn_sched_barrier(0);
-    const int mask = mask_of(t + 1);
+    const int bits = bits_of(t + 1);
     constexpr int n = c ? NC : NC + NSC;
     step(IC<1>{}, IC<c>{}, [&](auto I) __attribute__((always_inline)) {
       at_slot(I, typename S::Scale{}, IC<F>{},
               [&](auto X) __attribute__((always_inline)) { read_scale(nsa, nsb, IC<1 - c>{}, X); });
       at_slot(I, typename S::Read{}, IC<F>{},
               [&](auto X) __attribute__((always_inline)) { read_op(na, nbp, IC<0>{}, X); });
-      at_slot(I, typename S::Clear{}, IC<F>{},
-              [&](auto X) __attribute__((always_inline)) { clear_scale(mask, IC<1 - c>{}, X); });
+      at_slot(I, typename S::Take{}, IC<F>{},
+              [&](auto X) __attribute__((always_inline)) { take_scale(bits, IC<1 - c>{}, X); });
       at_slot(I, typename S::template Copy<n>{}, IC<n>{}, [&](auto X) __attribute__((always_inline)) {
         constexpr int x = decltype(X)::value;
         if constexpr (x < NC)
@@ -542,7 +550,7 @@ matmul_pipe(MatmulArgs p, TileMap map, int vec) {
       read_op(a0, b0, IC<0>{}, X);
       read_scale(sa0, sb0, IC<0>{}, X);
     }, std::make_integer_sequence<int, F>{});
-    static_for([&](auto X) __attribute__((always_inline)) { clear_scale(mask_of(0), IC<0>{}, X); },
+    static_for([&](auto X) __attribute__((always_inline)) { take_scale(bits_of(0), IC<0>{}, X); },
                std::make_integer_sequence<int, F>{});
     mfma_guard();
     int t = 0;

@@ -180,8 +180,13 @@ split_planes(const void* dY, int64_t ldy, int64_t T, int N, int groups, unsigned
 //  * The codes (token-contiguous, 64 bytes a feature and slice) and dY's
 //    rows (as in memory) go to LDS with 16-byte LDS-direct copies; the codes
 //    stay 8 bits wide there and are decoded on the way into the operand
-//    registers, 8 tokens of one block a lane: one scale each, four
-//    conversions, which run beside the matrix core.
+//    registers, four conversions an operand, which run beside the matrix
+//    core.  Lane group q takes tokens 16q + 8j .. + 7 of a slice in step j
+//    (any order common to both operands will do), so that a feature's codes
+//    for both steps are one 16-byte read and their scale, of block q/2, one
+//    byte.  (With 8 bytes a step, tokens 32j + 8q, those reads took 6 LDS
+//    cycles each, 4 of them in bank conflicts; 8192 tokens, 4096 x 4096:
+//    214 us.)
 //  * dY's operands want token-contiguous values of a column: the transpose
 //    read ds_read_b64_tr_b16 (in each group of 16 lanes, lane j gets element
 //    j%4 of the 8-byte pieces that lanes j/4 + 4t point at).  Its rows'
@@ -209,10 +214,15 @@ struct Tile {
   // scales, where zeros are wanted.
   static constexpr int S_STAGE = BM * 4 + MB * SF > 256 * NW ? BM * 4 + MB * SF : 256 * NW;
   static_assert(IA > 0 && IB > 0 && BM <= 64 * NW && B_ROW >= 256, "copies split over the waves");
-  __host__ __device__ static constexpr int b_swz(int k) { return (4 * (k % 4)) ^ ((k / 8) % 2); }
+  __host__ __device__ static constexpr int b_swz(int k) { return (4 * (k % 4)) ^ ((k / 16) % 2); }
   __host__ __device__ static constexpr int b_byte(int k, int n) {
     return k * B_ROW + 16 * ((n / 8) ^ b_swz(k)) + 2 * (n % 8);
   }
+  // Chunk q of feature row r: 16-byte reads serve rows 0-3 and 12-15 of one
+  // lane group with rows 4-11 of its neighbour, which this XOR (0, 3, 2, 1
+  // by fours of rows) sends to distinct banks.
+  __host__ __device__ static constexpr int a_swz(int r) { return (4 - r / 4 % 4) % 4; }
+  __host__ __device__ static constexpr int a_byte(int r, int q) { return r * A_ROW + 16 * (q ^ a_swz(r)); }
   // Slots among a step's NMMA instructions.
   __host__ __device__ static constexpr int a_slot(int f) { return f * NMMA / (4 * MB); }
   __host__ __device__ static constexpr int b_slot(int g) { return NMMA / 4 + g * NMMA / (2 * NB); }
@@ -291,7 +301,7 @@ wgrad_pipe(PipeArgs p, TileMap map, int vec) {
   };
 
   Copies<S> o;
-  const int qa = (l % 4) ^ (l / 16);
+  const int qa = (l % 4) ^ S::a_swz(l / 4);
 #pragma unroll
   for (int i = 0; i < S::IA; ++i) {
     const int row = 16 * (i * S::NW + wave) + l / 4;
@@ -309,15 +319,14 @@ wgrad_pipe(PipeArgs p, TileMap map, int vec) {
   }
   for (int i = tid; i < MB * S::SF / 4; i += 64 * S::NW)
     reinterpret_cast<unsigned*>(s0 + S::BM * 4)[i] = reinterpret_cast<unsigned*>(s1 + S::BM * 4)[i] = 0u;
-  int a_fb[2], b_fb[NB];
+  const int a_fb = S::a_byte(wm0 + r, q);
+  int b_fb[NB];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) a_fb[j] = swz_off(wm0 + r, 2 * j + q / 2, S::A_ROW) + 8 * (q % 2);
-#pragma unroll
-  for (int g = 0; g < NB; ++g) b_fb[g] = S::b_byte(8 * q + r / 4, wn0 + 16 * g + 4 * (r % 4));
-  const int s_fb = (wm0 + r) * 4;
+  for (int g = 0; g < NB; ++g) b_fb[g] = S::b_byte(16 * q + r / 4, wn0 + 16 * g + 4 * (r % 4));
+  const int s_fb = (wm0 + r) * 4 + q / 2;
 
   i32x4 fa[2][MB], fb[2][NB];
-  u32x2 raw[MB];
+  u32x4 raw[MB];  // a slice's codes and scales
   unsigned sc[MB];
   f32x4 acc[NB][MB];
 #pragma unroll
@@ -327,23 +336,25 @@ wgrad_pipe(PipeArgs p, TileMap map, int vec) {
   pin(acc);
   mfma_guard();
 
-  // Step j of a slice whose block 0 is `block` of the workgroup's, its
-  // scales the bytes 2c .. of their words.
-  auto read_a = [&](const uint8_t* la, const uint8_t* ls, int c, int j, int block, auto F) __attribute__((always_inline)) {
+  // Codes and scales of a slice whose block 0 is `block` of the workgroup's,
+  // its scales the bytes 2c .. of their words.
+  auto read_a = [&](const uint8_t* la, const uint8_t* ls, int c, int block, auto F) __attribute__((always_inline)) {
     constexpr int f = decltype(F)::value;
-    raw[f] = __builtin_bit_cast(u32x2, *(const lds_i32x2*)(la + a_fb[j] + f * 16 * S::A_ROW));
-    sc[f] = *(const lds_u8*)(ls + (BLOCK * (block + j) < bytes ? s_fb + 2 * c + j : S::BM * 4) + f * S::SF);
+    raw[f] = __builtin_bit_cast(u32x4, *(const lds_i32x4*)(la + a_fb + f * 16 * S::A_ROW));
+    sc[f] = *(const lds_u8*)(ls + (BLOCK * (block + q / 2) < bytes ? s_fb + 2 * c : S::BM * 4) + f * S::SF);
   };
   auto read_b = [&](int buf, const uint8_t* lb, int j, auto G) __attribute__((always_inline)) {
     constexpr int g = decltype(G)::value;
-    const uint8_t* b = lb + b_fb[g] + 32 * j * S::B_ROW;
+    const uint8_t* b = lb + b_fb[g] + 8 * j * S::B_ROW;
     const i32x2 lo = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)b));
     const i32x2 hi = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(b + 4 * S::B_ROW)));
     fb[buf][g] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3);
   };
-  auto decode = [&](int buf, auto F) __attribute__((always_inline)) {
+  // Step j's operand f.
+  auto decode = [&](int j, auto F) __attribute__((always_inline)) {
     constexpr int f = decltype(F)::value;
-    fa[buf][f] = __builtin_bit_cast(i32x4, decode8(raw[f], scale_float(sc[f])));
+    const u32x2 w = {j ? raw[f][2] : raw[f][0], j ? raw[f][3] : raw[f][1]};
+    fa[j][f] = __builtin_bit_cast(i32x4, decode8(w, scale_float(sc[f])));
   };
   auto step = [&](int cur, auto&& ra, auto&& rb, auto&& cp) __attribute__((always_inline)) {
     static_for([&](auto I) __attribute__((always_inline)) {
@@ -368,13 +379,12 @@ wgrad_pipe(PipeArgs p, TileMap map, int vec) {
     constexpr int c = decltype(C_)::value;
     uint8_t *la = c ? a1 : a0, *lb = c ? b1 : b0, *ls = c ? s1 : s0;
     uint8_t *na = c ? a0 : a1, *nbp = c ? b0 : b1, *ns = c ? s0 : s1;
-    step(0, [&](auto F) __attribute__((always_inline)) { read_a(la, ls, c, 1, 4 * pt + 2 * c, F); },
-         [&](auto G) __attribute__((always_inline)) { read_b(1, lb, 1, G); }, [](auto) {});
+    step(0, [](auto) {}, [&](auto G) __attribute__((always_inline)) { read_b(1, lb, 1, G); }, [](auto) {});
     loop_barrier();  // the next slice landed, stage c read by every wave
     __builtin_amdgcn_sched_barrier(0);
     const int k = 2 * S::BK * ptn + S::BK * c;
     const int left = (live ? len : 0) - k;
-    step(1, [&](auto F) __attribute__((always_inline)) { read_a(na, ns, c ^ 1, 0, c ? 4 * ptn : 4 * pt + 2, F); },
+    step(1, [&](auto F) __attribute__((always_inline)) { read_a(na, ns, c ^ 1, c ? 4 * ptn : 4 * pt + 2, F); },
          [&](auto G) __attribute__((always_inline)) { read_b(0, nbp, 0, G); },
          [&](auto Q) __attribute__((always_inline)) {
            copy_one<S, decltype(Q)::value>(A, Y, Sc, o, k, tnx * y_plane + k * (int64_t)y_row, 4 * ptn, (live ? bytes : 0) - k,
@@ -389,7 +399,7 @@ wgrad_pipe(PipeArgs p, TileMap map, int vec) {
                                       y_range(len - S::BK), a1, b1, s1, wave, qa);
     }, std::make_integer_sequence<int, S::LPS>{});
     loop_barrier();
-    static_for([&](auto F) __attribute__((always_inline)) { read_a(a0, s0, 0, 0, 0, F); },
+    static_for([&](auto F) __attribute__((always_inline)) { read_a(a0, s0, 0, 0, F); },
                std::make_integer_sequence<int, MB>{});
     static_for([&](auto G) __attribute__((always_inline)) { read_b(0, b0, 0, G); }, std::make_integer_sequence<int, NB>{});
     static_for([&](auto F) __attribute__((always_inline)) { decode(0, F); }, std::make_integer_sequence<int, MB>{});
