@@ -202,10 +202,10 @@ matmul_skinny(MatmulArgs p) {
         Eight<VT> v[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          const unsigned at = g + i < p.M && left > 0 ? (unsigned)((g + i) * (int)(p.ldx * VB) + VB * c) : OOB;
 #pragma unroll
           for (int h = 0; h < Eight<VT>::W / 4; ++h) {
-            const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, at + 16 * h, 0, 0));
+            const unsigned at = value_load<VB>(g + i, p.M, (unsigned)(p.ldx * VB), c, left, h);
+            const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, at, 0, 0));
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[i].w[4 * h + e] = x[e];
           }

@@ -6,6 +6,7 @@
 
 #include <utility>
 
+#include "mx_bounds.h"
 #include "mx_internal.h"
 
 namespace gemm {
@@ -24,8 +25,6 @@ typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
 typedef __attribute__((address_space(3))) unsigned lds_u32;
-
-constexpr unsigned OOB = 0x80000000u;  // offset past every descriptor's range
 
 template <int I>
 using IC = std::integral_constant<int, I>;
