@@ -6,7 +6,7 @@
 #include <stdint.h>
 
 #if defined(__HIP__)
-#define MX_HD __host__ __device__ __forceinline__
+#define MX_HD __host__ __device__ inline __attribute__((always_inline))
 #else
 #define MX_HD inline
 #endif
