@@ -1,7 +1,8 @@
 """Build libgemm.so (the HIP kernels and the C-ABI) for gfx950 with hipcc.
 
-Every source under ``csrc/`` is compiled to an object in ``_build/`` and
-linked into ``dense_gemm_row_amd/libgemm.so``.  Run as ``python -m
+Every source under ``csrc/`` is compiled to an object in ``_build/`` (the
+pipelined microscaled kernels to several, see PARTS) and linked into
+``dense_gemm_row_amd/libgemm.so``.  Run as ``python -m
 dense_gemm_row_amd.build`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -25,6 +26,27 @@ ARCH = "gfx950"
 
 SOURCES = ["gemm_api.hip", "splitk.hip", "sgemm_dl.hip", "sgemm_mfma.hip", "hgemm_mfma.hip", "hgemm_tr.hip", "sgemm_simt.hip",
            "mx_api.hip", "mx_quant.hip", "mx_matmul.hip", "mx_wgrad.hip"]
+# Sources compiled once for every set of definitions: their kernels are large
+# and the compiler's time grows faster than their number in a file (one 15 s,
+# two 39 s, four 115 s), so each object holds two (with and without the
+# epilogue) and the objects compile side by side.
+_TYPES = {"f32": 0, "f16": 1, "bf16": 2}
+PARTS = {
+    "mx_matmul_pipe.hip": [(f"{t}_{side}_{sc}", {"MX_DTYPE": d, "MX_SIDE": side, "MX_SC": sc})
+                           for side in (256, 128) for sc in (16, 4) for t, d in _TYPES.items()],
+    "mx_wgrad_pipe.hip": [(f"{t}_{side}", {"MX_DTYPE": d, "MX_SIDE": side}) for side in (256, 128) for t, d in _TYPES.items()],
+}
+
+
+def _stem(src: str) -> str:
+    return os.path.splitext(os.path.basename(src))[0]
+
+
+# (source, object name, definitions) of every object of the library.
+OBJECTS = [(src, _stem(src), ()) for src in SOURCES] + [
+    (src, f"{_stem(src)}_{name}", tuple(f"-D{k}={v}" for k, v in defs.items()))
+    for src, parts in PARTS.items() for name, defs in parts]
+PROBE_OBJECTS = [(src, _stem(src), ()) for src in PROBE_SOURCES]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
@@ -42,9 +64,13 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found; ROCm is required to build libgemm")
 
 
-def _compile(src: str, extra) -> str:
-    obj = os.path.join(BUILD_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+def _object(stem: str) -> str:
+    return os.path.join(BUILD_DIR, stem + ".o")
+
+
+def _compile(src: str, stem: str, defines, extra) -> str:
+    obj = _object(stem)
+    cmd = [hipcc(), *HIPCC_FLAGS, *defines, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{res.stdout}\n{res.stderr}")
@@ -67,12 +93,12 @@ def build(extra_flags=(), jobs: int | None = None, verbose: bool = False) -> str
     """Compile every source and link libgemm.so and libgemm_probe.so.
     Always rebuilds."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = SOURCES + PROBE_SOURCES
-    jobs = jobs or min(len(srcs), os.cpu_count() or 1)
+    todo = OBJECTS + PROBE_OBJECTS
+    jobs = jobs or min(len(todo), os.cpu_count() or 1)
     with cf.ThreadPoolExecutor(jobs) as ex:
-        objs = list(ex.map(lambda s: _compile(s, list(extra_flags)), srcs))
-    _link(objs[:len(SOURCES)], LIB)
-    _link(objs[len(SOURCES):], PROBE_LIB)
+        objs = list(ex.map(lambda o: _compile(*o, list(extra_flags)), todo))
+    _link(objs[:len(OBJECTS)], LIB)
+    _link(objs[len(OBJECTS):], PROBE_LIB)
     if verbose:
         print(f"built {LIB} and {PROBE_LIB}")
     return LIB
@@ -97,7 +123,7 @@ def build_host_sanitized(out: str, sanitizers=("address", "undefined")) -> str:
     device code is the regular build's; undefined behaviour is fatal),
     linked with the regular objects of the other sources into `out`.  Needs
     the objects of a previous build()."""
-    objs = [os.path.join(BUILD_DIR, os.path.splitext(s)[0] + ".o") for s in SOURCES if s != "gemm_api.hip"]
+    objs = [_object(stem) for src, stem, _ in OBJECTS if src != "gemm_api.hip"]
     missing = [o for o in objs if not os.path.exists(o)]
     if missing:
         raise RuntimeError(f"run build() first: missing {missing}")

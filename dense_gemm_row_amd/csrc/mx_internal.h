@@ -70,6 +70,17 @@ struct WgradPlan {
   int64_t bytes() const { return planes + partials; }
 };
 
+// The arguments of the pipelined kernel.
+struct WgradPipeArgs {
+  Coded x;
+  const uint16_t* y;  // bfloat16 planes
+  int64_t ldy, plane;
+  void* C;            // dW, or the first partial sum
+  int64_t ldc, c_stride;
+  int T, F, N, terms, chunk;
+  float alpha, beta;
+};
+
 hipError_t launch_quantize(int dtype, int format, bool trans, const QuantArgs& a, hipStream_t s);
 hipError_t launch_dequantize(int dtype, int format, bool trans, const DequantArgs& a, hipStream_t s);
 hipError_t launch_matmul(int c_dtype, const MatmulArgs& a, hipStream_t s);
@@ -79,6 +90,12 @@ bool values_fit(int a_dtype, const MatmulArgs& a);
 hipError_t launch_matmul_values(int a_dtype, int c_dtype, const MatmulArgs& a, hipStream_t s);
 hipError_t launch_wgrad(int y_dtype, int c_dtype, const WgradArgs& a, hipStream_t s);
 WgradPlan wgrad_plan(int y_dtype, int64_t T, int64_t F, int64_t N);
+// The pipelined kernels on tiles of SIDE x SIDE (mx_matmul_pipe.hip, scales
+// in pieces of SC bytes; mx_wgrad_pipe.hip), for C of type DT.
+template <int DT, int SIDE, int SC>
+hipError_t launch_matmul_pipe(const MatmulArgs& a, hipStream_t s);
+template <int DT, int SIDE>
+hipError_t launch_wgrad_pipe(const WgradPipeArgs& a, int splits, hipStream_t s);
 
 // Output types as template arguments: GEMM_DTYPE_F32 / _F16 / _BF16.
 template <int DT>

@@ -96,6 +96,16 @@ __device__ __forceinline__ void pin(f32x4 (&acc)[NB][MB]) {
 #endif
 }
 
+// Eight codes (tokens in order) of one block -> eight bfloat16 values.
+__device__ __forceinline__ u32x4 decode8(u32x2 w, float factor) {
+  u32x4 v;
+  v[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], factor, false));
+  v[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], factor, true));
+  v[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], factor, false));
+  v[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], factor, true));
+  return v;
+}
+
 // Stores of one 16-row block row of a wave's tile, through a buffer over C
 // (so without branches: what lies outside the matrix gets an offset past
 // the range).  Block nb's register i of lane l is element (l%16, 16nb +
