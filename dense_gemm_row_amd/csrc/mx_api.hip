@@ -27,7 +27,6 @@ constexpr int64_t kSizeLimit = 0x7fffffff;
 bool size_ok(int64_t n) { return n >= 0 && n <= kSizeLimit; }
 bool float_dtype(int d) { return d == GEMM_DTYPE_F32 || d == GEMM_DTYPE_F16 || d == GEMM_DTYPE_BF16; }
 int64_t dtype_bytes(int d) { return d == GEMM_DTYPE_F32 ? 4 : 2; }
-int64_t blocks_of(int64_t cols) { return (cols + BLOCK - 1) / BLOCK; }
 int64_t row_bytes(int format, int64_t cols) { return blocks_of(cols) * (format == GEMM_MX_E2M1 ? 16 : 32); }
 
 // A byte range [at, at + bytes): rows x row bytes at `ld` bytes.

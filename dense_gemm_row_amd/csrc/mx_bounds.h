@@ -16,6 +16,11 @@ namespace mx {
 
 constexpr unsigned OOB = 0x80000000u;  // offset past every descriptor's range
 
+// Sizes go up to 2^31 - 1, so roundings up are taken in 64 bits.
+MX_HD constexpr int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
+// Blocks of 32 of a row of `cols` values.
+MX_HD constexpr int64_t blocks_of(int64_t cols) { return ceil_div(cols, 32); }
+
 // A lane's eight values of type size VB, columns c .. c+7 of row `row`, come
 // in 16-byte loads (two of FP32, one of 16 bits): the byte offset of load h.
 // `left` columns of the matrix are at c and beyond.  A load none of whose

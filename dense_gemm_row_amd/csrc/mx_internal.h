@@ -5,6 +5,7 @@
 
 #include "gemm_internal.h"
 #include "gemm_mx.h"
+#include "mx_bounds.h"
 
 namespace gemm {
 

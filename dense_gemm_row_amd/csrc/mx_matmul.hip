@@ -57,7 +57,7 @@ matmul_direct(MatmulArgs p, int tiles_n, int64_t tiles) {
   __shared__ __attribute__((aligned(16))) float sums[W][BM][BN];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane % 16, q = lane / 16;
-  const int nb = (p.K + BLOCK - 1) / BLOCK;
+  const int nb = (int)blocks_of(p.K);
   const int steps = (nb + 3) / 4;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t m0 = tile / tiles_n * BM, n0 = tile % tiles_n * BN;
@@ -122,8 +122,8 @@ matmul_direct(MatmulArgs p, int tiles_n, int64_t tiles) {
 
 template <int DT, int MT, int NT, int W, int U>
 hipError_t launch_direct(const MatmulArgs& a, hipStream_t stream) {
-  const int tiles_n = (a.N + 16 * NT - 1) / (16 * NT);
-  const int64_t tiles = (int64_t)tiles_n * ((a.M + 16 * MT - 1) / (16 * MT));
+  const int tiles_n = (int)ceil_div(a.N, 16 * NT);
+  const int64_t tiles = tiles_n * ceil_div(a.M, 16 * MT);
   const int64_t most = 1 << 22;  // work-items of a grid: below 2^32
   hipLaunchKernelGGL((matmul_direct<DT, MT, NT, W, U>), dim3((unsigned)(tiles < most ? tiles : most)), dim3(64 * W),
                      0, stream, a, tiles_n, tiles);
@@ -279,7 +279,7 @@ bool skinny_ok(const MatmulArgs& a) {
 
 template <int DT, int AT>
 hipError_t launch_skinny(const MatmulArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.N + 15) / 16));
+  const dim3 grid((unsigned)ceil_div(a.N, 16));
   // One turn of every wave, where 16 can do it.
   if (a.K > 128 * kSkinnyDepth * kSkinnyWaves)
     hipLaunchKernelGGL((matmul_skinny<DT, AT, 16>), grid, dim3(64 * 16), 0, stream, a);
@@ -302,7 +302,7 @@ bool pipe_ok(const MatmulArgs& a) {
   const int64_t far = (int64_t)0x7fffffff / 256 - 4096;
   return a.K > 0 && (uintptr_t)a.a.scales % 4 == 0 && a.a.lds % 4 == 0 && (uintptr_t)a.b.scales % 4 == 0 &&
          a.b.lds % 4 == 0 && a.a.ldq < far && a.b.ldq < far && a.a.lds < far && a.b.lds < far && a.ldc < far / 4 &&
-         (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128) < (1 << 23);
+         ceil_div(a.M, 128) * ceil_div(a.N, 128) < (1 << 23);
 }
 
 template <int DT>
@@ -314,7 +314,7 @@ hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
   // 256 x 256 tiles reuse each operand byte twice as often, 128 x 128 ones
   // fill the 256 CUs with a quarter of the outputs (4096^3: 39 against
   // 50 us; 2048^3: 19 against 10 us).
-  const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const int64_t tiles = ceil_div(a.M, 256) * ceil_div(a.N, 256);
   if (tiles >= 192) return launch_pipe<DT, 256>(a, stream);
   return launch_pipe<DT, 128>(a, stream);
 }

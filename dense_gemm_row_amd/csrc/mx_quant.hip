@@ -441,7 +441,7 @@ hipError_t launch_quantize(int dtype, int format, bool trans, const QuantArgs& a
     const dim3 block(kThreads);
     QuantArgs a = args;
     if (!trans) {
-      const int chunks = (a.cols + BLOCK - 1) / BLOCK * 4;
+      const int chunks = (int)(4 * blocks_of(a.cols));
       const bool many = unrolled(a.rows, chunks);
       return slice_rows(args.rows, chunks, many ? kUnroll : 1, [&](dim3 grid, const RowGrid& g, int64_t r0, int n) {
         a.X = static_cast<const unsigned char*>(args.X) + r0 * a.ldx * kBytes<DT>;
@@ -484,7 +484,7 @@ hipError_t launch_dequantize(int dtype, int format, bool trans, const DequantArg
     const dim3 block(kThreads);
     DequantArgs a = args;
     if (!trans) {
-      const int chunks = (a.cols + 7) / 8;
+      const int chunks = (int)ceil_div(a.cols, 8);
       const bool many = unrolled(a.rows, chunks);
       return slice_rows(args.rows, chunks, many ? kUnroll : 1, [&](dim3 grid, const RowGrid& g, int64_t r0, int n) {
         a.X = static_cast<unsigned char*>(args.X) + r0 * a.ldx * kBytes<DT>;

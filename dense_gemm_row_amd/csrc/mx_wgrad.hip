@@ -233,8 +233,8 @@ hipError_t launch_planned(const WgradArgs& a, const WgradPlan& w, hipStream_t st
 
 template <int YT, int CT>
 hipError_t launch_general(const WgradArgs& a, hipStream_t stream) {
-  const int tiles_n = (a.N + 63) / 64;
-  const int64_t tiles = (int64_t)tiles_n * ((a.F + 63) / 64);
+  const int tiles_n = (int)ceil_div(a.N, 64);
+  const int64_t tiles = tiles_n * ceil_div(a.F, 64);
   const int64_t most = 1 << 22;  // work-items of a grid: below 2^32
   hipLaunchKernelGGL((wgrad_general<YT, CT>), dim3((unsigned)(tiles < most ? tiles : most)), dim3(256), 0, stream, a,
                      tiles_n, tiles);

@@ -1,6 +1,6 @@
 """The index arithmetic of the microscaled operators (csrc/mx_bounds.h, the
 header the kernels and their launches include), compiled for the CPU and
-evaluated there: which bytes a load touches.  CPU only."""
+evaluated there: counts of blocks, and which bytes a load touches.  CPU only."""
 import ctypes
 import os
 import shutil
@@ -14,6 +14,7 @@ OOB = 0x80000000
 SHIM = """
 #include "mx_bounds.h"
 using namespace gemm::mx;
+extern "C" int64_t blocks(int64_t cols) { return blocks_of(cols); }
 extern "C" unsigned value_load_4(int row, int rows, unsigned row_bytes, int c, int left, int h) {
   return value_load<4>(row, rows, row_bytes, c, left, h);
 }
@@ -40,7 +41,13 @@ def bounds(tmp_path_factory):
     for name in ("value_load_4", "value_load_2"):
         getattr(lib, name).restype = ctypes.c_uint
         getattr(lib, name).argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_uint] + [ctypes.c_int] * 3
+    lib.blocks.restype, lib.blocks.argtypes = ctypes.c_int64, [ctypes.c_int64]
     return lib
+
+
+@pytest.mark.parametrize("cols", [0, 1, 32, 33, 2 ** 31 - 33, 2 ** 31 - 32, 2 ** 31 - 31, 2 ** 31 - 1])
+def test_blocks_of_a_row(bounds, cols):
+    assert bounds.blocks(cols) == -(-cols // 32)
 
 
 @pytest.mark.parametrize("size", [2, 4])
