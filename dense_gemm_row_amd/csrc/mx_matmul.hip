@@ -264,11 +264,12 @@ matmul_skinny(MatmulArgs p) {
 }
 
 // What it takes: 16 rows of every operand within 31 bits, scales in 4-byte
-// words, and (values) rows of whole 16 bytes.
+// words, fewer than 2^22 workgroups (of up to 1024 work-items: a grid's have
+// to stay below 2^32), and (values) rows of whole 16 bytes.
 template <int AT>
 bool skinny_ok(const MatmulArgs& a) {
   const int64_t far = 1 << 26;
-  if (a.K <= 0 || a.M > 16 || a.N > (int64_t)16 << 22 || a.b.ldq >= far || a.b.lds >= far || a.b.lds % 4 != 0 ||
+  if (a.K <= 0 || a.M > 16 || a.N > far - 16 || a.b.ldq >= far || a.b.lds >= far || a.b.lds % 4 != 0 ||
       (uintptr_t)a.b.scales % 4 != 0)
     return false;
   if constexpr (AT < 0)

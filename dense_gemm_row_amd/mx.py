@@ -335,7 +335,7 @@ def matmul(a, b: MxTensor, out=None, out_dtype=None, alpha: float = 1.0, beta: f
         return out
     x, coded, row = a.data_ptr(), b._args(), lda * a.element_size()
     # A decoding step's few rows need no workspace (the header's conditions).
-    inside = (M <= 16 and (x | row) % 16 == 0 and (coded[2] | coded[3]) % 4 == 0 and N <= _FAR
+    inside = (M <= 16 and (x | row) % 16 == 0 and (coded[2] | coded[3]) % 4 == 0 and N <= _FAR - 16
               and max(row, coded[1], coded[3]) < _FAR)
     need = 0 if inside else lib().gemm_mx_matmul_values_workspace_bytes(M, K)
     ws = on.empty(need, _torch.uint8) if need > 0 else None

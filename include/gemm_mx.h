@@ -102,7 +102,7 @@ gemm_status_t gemm_mx_matmul(int32_t c_dtype, int64_t M, int64_t N, int64_t K,
  * give one after the other.  Up to 16 rows, a decoding step's, are encoded
  * inside the product, in one launch, if X's rows are 16-byte aligned, Bt's
  * scale rows 4-byte aligned, every row stride below 2^26 bytes and N at most
- * 2^26; `workspace` may be NULL then.  Otherwise the codes go through it
+ * 2^26 - 16; `workspace` may be NULL then.  Otherwise the codes go through it
  * (gemm_mx_matmul_values_workspace_bytes bytes, 16-byte aligned, not
  * overlapping the operands; too small a one -> INVALID_ARG).
  */

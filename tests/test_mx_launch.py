@@ -61,6 +61,27 @@ def test_products_of_far_sizes(dry, far, near, lds):
             assert one.grid[0] == min(one.arg[1], 1 << 22)
 
 
+@pytest.mark.parametrize("n", [2 ** 26 - 17, 2 ** 26 - 16, 2 ** 26 - 15, 2 ** 26 - 1, 2 ** 26, 2 ** 26 + 1])
+@pytest.mark.parametrize("k", [4096, 4097])
+def test_few_rows_and_very_many_columns(dry, n, k):
+    one, = product(dry, 16, n, k, whole(up(k, 32), 4))
+    assert one.grid[0] >= min(up(n, 16), 1 << 22)
+
+
+@pytest.mark.parametrize("n", [2 ** 26 - 16, 2 ** 26 - 15, 2 ** 26])
+def test_few_rows_of_values_and_very_many_columns(dry, n):
+    """The documented border: one launch without a workspace up to it."""
+    k = 8192
+    args = (BF16, BF16, 16, n, k, X, k, B, k // 2, BS, k // 32, C, n)
+    if n <= 2 ** 26 - 16:
+        one, = launched(dry, "gemm_mx_matmul_values", *args, None, 0, None, None)
+        assert one.kernel == "matmul_skinny" and one.grid[0] == up(n, 16)
+    else:
+        assert dry("gemm_mx_matmul_values", *args, None, 0, None, None) == (gemm.GEMM_ERR_INVALID_ARG, [])
+        first, second = launched(dry, "gemm_mx_matmul_values", *args, W, 1 << 20, None, None)
+        assert first.kernel == "quantize_rows" and second.kernel == "matmul_direct"
+
+
 @pytest.mark.parametrize("name, step", [("gemm_mx_quantize", 32), ("gemm_mx_dequantize", 8)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("pad", [0, 1, 8])
