@@ -238,6 +238,11 @@ def _out_dtype(dtype, default, name):
     return dtype
 
 
+def _scale_row(blocks: int) -> int:
+    unit = 4 if blocks < 16 else 16
+    return -(-blocks // unit) * unit
+
+
 def empty(rows: int, cols: int, fmt: str, device) -> MxTensor:
     """An uninitialised coded matrix; scale rows are a multiple of 4 bytes, or
     of 16 where they are that long (the widest pieces the kernels copy)."""
@@ -248,11 +253,11 @@ def empty(rows: int, cols: int, fmt: str, device) -> MxTensor:
     blocks = -(-cols // BLOCK)
     q = MxTensor.__new__(MxTensor)  # (as the checks of __init__ would have it)
     q.codes = _torch.empty((rows, blocks * BLOCK_BYTES[fmt]), dtype=_torch.uint8, device=device)
-    unit = 4 if blocks < 16 else 16
-    if blocks % unit == 0:
+    width = _scale_row(blocks)
+    if width == blocks:
         q.scales = _torch.empty((rows, blocks), dtype=_torch.uint8, device=device)
     else:
-        q.scales = _torch.empty_strided((rows, blocks), (-(-blocks // unit) * unit, 1), dtype=_torch.uint8, device=device)
+        q.scales = _torch.empty_strided((rows, blocks), (width, 1), dtype=_torch.uint8, device=device)
     q.cols, q.fmt = cols, fmt
     return q
 
@@ -412,17 +417,29 @@ def _make_linear():
                 raise TypeError("x and w must have one type")
             if wq.shape != (w.shape[1], w.shape[0]):
                 raise ValueError("wq is not the coded form of w.T")
-            ctx.kept = checkpoint(x) if ctx.needs_input_grad[1] else None
-            ctx.save_for_backward(w)
-            return matmul(x, wq, out_dtype=x.dtype)
+            y = matmul(x, wq, out_dtype=x.dtype)
+            codes = scales = None
+            if ctx.needs_input_grad[1]:
+                # (The scales' rows with their padding: a hook that copies a
+                # saved tensor keeps its shape, but no padding in strides.)
+                T, F = x.shape
+                blocks = -(-T // BLOCK)
+                codes = torch.empty((F, blocks * BLOCK_BYTES[E4M3]), dtype=torch.uint8, device=x.device)
+                scales = torch.empty((F, _scale_row(blocks)), dtype=torch.uint8, device=x.device)
+                checkpoint(x, out=MxTensor(codes, scales[:, :blocks], T, E4M3))
+            ctx.save_for_backward(w, codes, scales)
+            return y
 
         @staticmethod
         def backward(ctx, dy):
-            w, = ctx.saved_tensors
+            w, codes, scales = ctx.saved_tensors
             if dy.dim() == 2 and dy.shape[1] > 1 and dy.stride(1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):
                 dy = dy.contiguous()  # an expanded or transposed gradient
             dx = gemm.matmul(dy, w, b_transposed=True) if ctx.needs_input_grad[0] else None
-            dw = weight_grad(ctx.kept, dy, out_dtype=w.dtype) if ctx.needs_input_grad[1] else None
+            dw = None
+            if ctx.needs_input_grad[1]:
+                T = dy.shape[0]
+                dw = weight_grad(MxTensor(codes, scales[:, :-(-T // BLOCK)], T, E4M3), dy, out_dtype=w.dtype)
             return dx, dw, None
 
     return Linear
