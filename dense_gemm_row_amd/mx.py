@@ -431,6 +431,7 @@ def _make_linear():
             return y
 
         @staticmethod
+        @torch.autograd.function.once_differentiable  # (the kernels record no graph)
         def backward(ctx, dy):
             w, codes, scales = ctx.saved_tensors
             if dy.dim() == 2 and dy.shape[1] > 1 and dy.stride(1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):

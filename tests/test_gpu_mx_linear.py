@@ -48,3 +48,14 @@ def test_frozen_weight_saves_no_checkpoint():
     assert [t.shape for t in packed] == [w.shape]
     y.backward(dy)
     assert x.grad is not None and w.grad is None
+
+
+def test_second_derivative_is_refused():
+    """The kernels record no graph, so a derivative of the gradients would
+    lack their terms."""
+    x, w, _ = layer("f32")
+    y = mx.linear(x, w, mx.quantize(w.detach(), transposed=True))
+    dx, dw = torch.autograd.grad((y * y).sum(), (x, w), create_graph=True)
+    for loss in ((dx * x).sum(), (dw * w).sum()):
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            loss.backward(retain_graph=True)
