@@ -390,15 +390,21 @@ def weight_grad(kept: MxTensor, dy, out=None, out_dtype=None, alpha: float = 1.0
     return out
 
 
+def _row_major(t) -> bool:
+    rows, cols = t.shape
+    return (cols <= 1 or t.stride(1) == 1) and (rows <= 1 or t.stride(0) >= cols)
+
+
 _Linear = None
 
 
 def linear(x, w, wq: MxTensor):
     """y = x @ w for training: the forward product in 4 bits, the backward
     pass from 8-bit activations.  x is tokens x K, w the K x N weight (any of
-    float32, float16, bfloat16; x of the same type), wq its coded form
-    ``quantize(w, transposed=True)``, remade by the caller after each weight
-    update.  Saved for backward are w and the 8-bit checkpoint of x, not x.
+    float32, float16, bfloat16; x of the same type; row-major or the transpose
+    of a row-major N x K parameter), wq its coded form
+    ``quantize(w, transposed=True)`` (of such a parameter:
+    ``quantize(parameter)``), remade by the caller after each weight update.  Saved for backward are w and the 8-bit checkpoint of x, not x.
     Gradients (straight through the quantisation): dx = dy @ w.T and dw =
     x^.T @ dy with x^ the checkpoint's values, both in w's type."""
     global _Linear
@@ -417,6 +423,9 @@ def _make_linear():
                 raise TypeError("x and w must have one type")
             if wq.shape != (w.shape[1], w.shape[0]):
                 raise ValueError("wq is not the coded form of w.T")
+            if not (_row_major(w) or _row_major(w.t())):
+                raise ValueError("w must be row-major or the transpose of a row-major tensor")
+            _same_device(x, w)
             y = matmul(x, wq, out_dtype=x.dtype)
             codes = scales = None
             if ctx.needs_input_grad[1]:
@@ -434,10 +443,11 @@ def _make_linear():
         @torch.autograd.function.once_differentiable  # (the kernels record no graph)
         def backward(ctx, dy):
             w, codes, scales = ctx.saved_tensors
-            if dy.dim() == 2 and dy.shape[1] > 1 and dy.stride(1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):
+            if not _row_major(dy):
                 dy = dy.contiguous()  # an expanded or transposed gradient
-            dx = gemm.matmul(dy, w, b_transposed=True) if ctx.needs_input_grad[0] else None
-            dw = None
+            dx = dw = None
+            if ctx.needs_input_grad[0]:
+                dx = gemm.matmul(dy, w, b_transposed=True) if _row_major(w) else gemm.matmul(dy, w.t())
             if ctx.needs_input_grad[1]:
                 T = dy.shape[0]
                 dw = weight_grad(MxTensor(codes, scales[:, :-(-T // BLOCK)], T, E4M3), dy, out_dtype=w.dtype)

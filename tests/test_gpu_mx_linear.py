@@ -59,3 +59,27 @@ def test_second_derivative_is_refused():
     for loss in ((dx * x).sum(), (dw * w).sum()):
         with pytest.raises(RuntimeError, match="once_differentiable"):
             loss.backward(retain_graph=True)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("shape", [(70, 96, 40), (1, 33, 1), (5, 1, 7), (0, 64, 8)])
+def test_weight_of_either_orientation(kind, shape):
+    """w as the transpose of a row-major N x K parameter gives what its
+    row-major copy gives."""
+    x, w, dy = layer(kind, *shape)
+    param = w.detach().t().contiguous().requires_grad_(True)
+    wq = mx.quantize(param.detach())
+    assert torch.equal(wq.codes, mx.quantize(w.detach(), transposed=True).codes)
+    y = mx.linear(x, w, wq)
+    y.backward(dy)
+    x2 = x.detach().clone().requires_grad_(True)
+    y2 = mx.linear(x2, param.t(), wq)
+    y2.backward(dy)
+    assert torch.equal(y, y2)
+    assert torch.equal(param.grad.t(), w.grad)
+    # dx: the same sums, maybe in another order: n additions in FP32 and the
+    # result's rounding, on both sides.
+    size = dy.double().abs() @ w.detach().double().abs().t()
+    half = torch.finfo(TYPES[kind]).eps / 2
+    n = shape[2]
+    assert bool(((x.grad.double() - x2.grad.double()).abs() <= 2 * ((n + 8) * 2.0 ** -23 + half) * size).all())
