@@ -7,6 +7,7 @@ import pytest
 
 from dense_gemm_row_amd import gemm
 from tests.mx_dry_run import compile_dry
+from tests.mx_sizes import LARGE_GRADS, LARGE_PRODUCTS
 
 TOP = 2 ** 31 - 1
 F32, F16, BF16 = gemm.DTYPE_F32, gemm.DTYPE_F16, gemm.DTYPE_BF16
@@ -118,3 +119,26 @@ def test_gradients_of_far_sizes(dry, far):
         assert one.kernel == "wgrad_general"
         assert one.arg[0] == up(n, 64) and one.arg[1] == up(n, 64) * up(f, 64)
         assert one.grid[0] == min(one.arg[1], 1 << 22)
+
+
+@pytest.mark.parametrize("m, n, k", LARGE_PRODUCTS)
+@pytest.mark.parametrize("lds", [4, 16])
+def test_large_tile_of_products(dry, m, n, k, lds):
+    one, = product(dry, m, n, k, whole(up(k, 32), 16) + lds % 16)
+    assert one.kernel == "matmul_pipe" and f"ELi{lds}EEE" in one.name.decode()
+    assert one.grid[0] == up(m, 256) * up(n, 256)
+
+
+@pytest.mark.parametrize("t, f, n", LARGE_GRADS)
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_large_tile_of_gradients(dry, t, f, n, dtype):
+    chunks = LARGE_GRADS[t, f, n][dtype != BF16]
+    need = dry.lib.gemm_mx_wgrad_workspace_bytes(dtype, t, f, n)
+    launches = launched(dry, "gemm_mx_wgrad", dtype, F32, t, f, n, A, whole(t, 32), AS, whole(up(t, 32), 4), X, n, C, n, 1.0, 0.0,
+                        W, need, None)
+    pipe = [one for one in launches if one.kernel == "wgrad_pipe"][0]
+    assert ("Li256ELi256" in pipe.name.decode()) == (chunks > 0)
+    if chunks:
+        assert tuple(pipe.grid) == (up(f, 256) * up(n, 256), chunks)
+        assert (launches[-1].kernel == "reduce_partials") == (chunks > 1)
+    assert (launches[0].kernel == "split_planes") == (dtype != BF16 or n % 8 != 0)
