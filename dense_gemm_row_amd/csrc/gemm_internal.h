@@ -248,9 +248,14 @@ __host__ __device__ inline void tile_of_block(int b, const TileMap& t, int& tm, 
 // ---------------------------------------------------------------------------
 // LDS model used by the layout derivations (measured on gfx950): 64 banks of
 // 4 bytes.  A wave's ds_read/ds_write of W bytes per lane is serviced in
-// groups of 256/W consecutive lanes (16 lanes for 16-byte accesses); an
-// access group is conflict-free when its lanes touch distinct banks (equal
-// addresses broadcast).
+// groups of 256/W lanes (16 lanes for 16-byte accesses); an access group is
+// conflict-free when its lanes touch distinct banks (equal addresses
+// broadcast).  The layouts here are derived with groups of consecutive lanes.
+// The counters fit another grouping of 16-byte reads better, lanes 0-3 and
+// 12-15 of one 16-lane row with lanes 4-11 of its neighbour: 64-byte rows
+// read by 16 lanes at chunk q ^ (r/4)%4, free by the first rule, count 4
+// conflict cycles of 8, and at chunk q ^ (4 - r/4)%4, free by the second,
+// none.  128-byte rows at chunk q ^ (r/2)%8 are free by both.
 // ---------------------------------------------------------------------------
 constexpr int kLdsBanks = 64;
 

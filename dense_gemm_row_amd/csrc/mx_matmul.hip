@@ -133,7 +133,7 @@ hipError_t launch_direct(const MatmulArgs& a, hipStream_t stream) {
 // Up to 16 rows: 16 columns a workgroup, its W waves taking turns along k,
 // four steps (512 k) each, all of whose loads are issued at once.  The
 // operand layout has four lanes a row, 64 bytes of it per load, which the
-// memory serves badly (16 x 11008 x 4096: 14 us against 10); so the weights'
+// memory serves badly (16 x 11008 x 4096: 14 us against 11); so the weights'
 // codes go through LDS, copied 256 bytes of a row at a time (LDS-direct,
 // wave-private, chunk c of row r at c ^ r: conflict-free reads), and their
 // scales, 16 bytes of a row, with one copy.  What lies outside the matrix
@@ -313,8 +313,13 @@ hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
                             : launch_direct<DT, 1, 1, kSkinnyWaves, kSkinnyDepth>(a, stream);
   if (!pipe_ok(a)) return launch_direct<DT, 4, 4, 4, 1>(a, stream);
   // 256 x 256 tiles reuse each operand byte twice as often, 128 x 128 ones
-  // fill the 256 CUs with a quarter of the outputs (4096^3: 39 against
-  // 50 us; 2048^3: 19 against 10 us).
+  // fill the 256 CUs with a quarter of the outputs.  Large against small
+  // tiles, K = 4096, bfloat16, by the number of large ones: 64 (2048^2) 28
+  // against 15.5 us, 100 29 against 22, 144 35 against 40, 196 56 against 64,
+  // 256 (4096^2) 37 against 45, 289 102 against 86, 361 102 against 98, 400
+  // 80 against 88, 484 70 against 83.  (The border is not at the best place:
+  // 144 would do with the large ones, and 257 to about 380 of them, a second
+  // and mostly empty round, with the small.)
   const int64_t tiles = ceil_div(a.M, 256) * ceil_div(a.N, 256);
   if (tiles >= 192) return launch_pipe<DT, 256>(a, stream);
   return launch_pipe<DT, 128>(a, stream);

@@ -18,7 +18,7 @@ namespace {
 //    read serves 16 lanes at a time, rows 0-3 and 12-15 of an even lane group
 //    with rows 4-11 of the next (or the other way round); with step j's chunk
 //    of group q at position (4j + q) ^ (r/2)%8 of row r's 128 bytes, those
-//    hit distinct banks.
+//    hit distinct banks (counted alone: no conflict cycle).
 //  * Scales go to LDS for two slices at a time, 16 bytes of a row (SC = 16:
 //    one copy a wave and operand; SC = 4, for scale rows that are only 4-byte
 //    aligned, four).  A slice's two steps take blocks 2q and 2q + 1 for lane
@@ -26,8 +26,9 @@ namespace {
 //    word that two groups share), and the instruction picks the byte.  A
 //    bit-field extraction takes them out of the word and clears those past
 //    the matrix' blocks, which may be anything (255 would be NaN).
-//    (8192^3: 273 us with 8 bytes a slice in 4-byte copies and a byte read
-//    for each step.)
+//    (8192^3: 244 us; 273 us with 8 bytes a slice in 4-byte copies and a byte
+//    read for each step.)  Those reads, of words 16 bytes apart, are the
+//    loop's bank conflicts: 2 of each one's 4 LDS cycles, 17 % of all.
 //  * A k step is MB x NB matrix instructions in a fixed order; the next
 //    step's operand reads and the copies of the slice after next are placed
 //    between them.  One barrier per slice, before its last step (whose

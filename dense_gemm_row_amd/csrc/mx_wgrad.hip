@@ -270,8 +270,10 @@ hipError_t launch(int c_dtype, const WgradArgs& a, hipStream_t stream) {
 // full: a slice (64 tokens) of a 256 x 256 tile 1.2 on an idle card to 1.7
 // on a full one, of a 128 x 128 tile 0.56 for each that shares a CU; a launch 4; the
 // partial sums, written and read, 8 TB/s.  (8192 tokens, 4096 x 4096: 214 us
-// on one 256 x 256 tile a CU, 288 on 128 x 128 ones; 16384 tokens, 1024 x
-// 1024: 51 us in 8 chunks, 152 in one.)
+// on one 256 x 256 tile a CU, 288 on 128 x 128 ones.  16384 tokens, 1024 x
+// 1024, on 128 x 128 tiles: 152 us in one chunk, 57 in the 4 that the model
+// picks, 51 in 8.  It prices those too high: two workgroups on a CU overlap,
+// and it charges each the whole slice.)
 WgradPlan wgrad_plan(int y_dtype, int64_t T, int64_t F, int64_t N) {
   WgradPlan best;
   const int64_t cap = (int64_t)1 << 23;  // workgroups of a grid, and columns within a tile's 31 bits

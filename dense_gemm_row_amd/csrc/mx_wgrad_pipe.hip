@@ -21,14 +21,16 @@ namespace {
 //    core.  Lane group q takes tokens 16q + 8j .. + 7 of a slice in step j
 //    (any order common to both operands will do), so that a feature's codes
 //    for both steps are one 16-byte read and their scale, of block q/2, one
-//    byte.  (With 8 bytes a step, tokens 32j + 8q, those reads took 6 LDS
-//    cycles each, 4 of them in bank conflicts; 8192 tokens, 4096 x 4096:
-//    214 us.)
+//    byte.  (8192 tokens, 4096 x 4096: 204 us; 214 us with 8 bytes a step,
+//    tokens 32j + 8q, whose reads took 6 LDS cycles each, 4 of them in bank
+//    conflicts.)
 //  * dY's operands want token-contiguous values of a column: the transpose
 //    read ds_read_b64_tr_b16 (in each group of 16 lanes, lane j gets element
 //    j%4 of the 8-byte pieces that lanes j/4 + 4t point at).  Its rows'
-//    16-byte chunks are XORed by 4(k%4) + (k/8)%2, so that the rows and
-//    k runs of one read hit distinct banks.
+//    16-byte chunks are XORed by 4(k%4) + (k/16)%2: step j's rows are 8j
+//    further, which must not change the XOR.  2 of each transpose read's 4
+//    LDS cycles are still bank conflicts, 36 % of the kernel's LDS cycles;
+//    the codes' and scales' reads have none.
 //  * Scales: one 4-byte word a feature (four blocks) with every slice;
 //    blocks past the tokens read zeros kept behind them.
 //  * The terms of dY are further tokens: the slices run over the tokens of

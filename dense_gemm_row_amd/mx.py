@@ -117,7 +117,9 @@ class MxTensor:
     """A coded matrix (the format of include/gemm_mx.h): ``codes`` (uint8,
     rows x 16 or 32 bytes a block) and ``scales`` (uint8, rows x blocks), for
     ``cols`` values a row.  Both may be views with a larger row stride; codes
-    need 16-byte alignment and a row stride of a multiple of 16."""
+    need 16-byte alignment and a row stride of a multiple of 16.  Products are
+    several times faster where the scales' row stride is a multiple of 4 bytes
+    too (`empty` and `quantize` make it so; a contiguous copy may not be)."""
     __slots__ = ("codes", "scales", "cols", "fmt")
 
     def __init__(self, codes, scales, cols: int, fmt: str = E2M1):
@@ -366,7 +368,9 @@ def restore(kept: MxTensor, dtype=None, out=None, stream=None):
 def weight_grad(kept: MxTensor, dy, out=None, out_dtype=None, alpha: float = 1.0, beta: float = 0.0, stream=None):
     """dW = alpha * x.T @ dy + beta * out from x's checkpoint (features x
     tokens) and dy (tokens x N): features x N, float32 unless out or
-    out_dtype says otherwise.  beta = 1 accumulates over micro-batches."""
+    out_dtype says otherwise.  beta = 1 accumulates over micro-batches.  (A
+    bfloat16 dy with N a multiple of 8 should have rows on 16 bytes; a slice
+    that has not is up to nine times slower than its contiguous copy.)"""
     _coded(kept, "kept", E4M3)
     y_dtype, rows, N, ldy = _dense(dy, "dy")
     _same_device(kept, dy)
@@ -404,9 +408,11 @@ def linear(x, w, wq: MxTensor):
     float32, float16, bfloat16; x of the same type; row-major or the transpose
     of a row-major N x K parameter), wq its coded form
     ``quantize(w, transposed=True)`` (of such a parameter:
-    ``quantize(parameter)``), remade by the caller after each weight update.  Saved for backward are w and the 8-bit checkpoint of x, not x.
-    Gradients (straight through the quantisation): dx = dy @ w.T and dw =
-    x^.T @ dy with x^ the checkpoint's values, both in w's type."""
+    ``quantize(parameter)``), remade by the caller after each weight update.
+    Saved for backward are w and the 8-bit checkpoint of x, not x.
+    Gradients: dx = dy @ w.T with w itself, not its 4-bit values, and dw =
+    x^.T @ dy with x^ the 8-bit checkpoint's values, not the 4-bit ones that
+    the product took; both in w's type.  There is no second derivative."""
     global _Linear
     if _Linear is None:
         _Linear = _make_linear()

@@ -90,6 +90,15 @@ gemm_status_t gemm_mx_dequantize(int32_t dtype, int32_t format, int32_t trans,
  * rounded once.  epi NULL: C = A x Bt^T (C is not read); otherwise as
  * gemm_*_epi (beta == 0: C is not read; bias overlapping C -> ALIAS).
  * K == 0: the empty sum.
+ *
+ * Speed: the fast kernels take scales (A's and Bt's) that are 4-byte aligned
+ * with rows of a multiple of 4 bytes, best of 16; the bytes behind a row's
+ * blocks may be anything.  Other scales, code rows 2^23 - 2^12 bytes apart or
+ * more (16 rows or fewer: 2^26) and rows of C 2^21 - 2^10 elements apart or
+ * more take a general kernel (8192 x 8192 x 8160 with rows of 255 scales: 1190 us
+ * against 296 with rows of 256).
+ * 16-byte groups of X's rows and words of scales are read whole where one of
+ * their values is in the matrix; what lies behind the matrix is not used.
  */
 gemm_status_t gemm_mx_matmul(int32_t c_dtype, int64_t M, int64_t N, int64_t K,
                              const uint8_t *A, int64_t lda, const uint8_t *As, int64_t ldas,
@@ -98,8 +107,10 @@ gemm_status_t gemm_mx_matmul(int32_t c_dtype, int64_t M, int64_t N, int64_t K,
 
 /*
  * The same product with A = X quantised to E2M1 on the way (X is M x K of
- * type a_dtype: F32, F16, BF16): what gemm_mx_quantize and gemm_mx_matmul
- * give one after the other.  Up to 16 rows, a decoding step's, are encoded
+ * type a_dtype: F32, F16, BF16): the sums that gemm_mx_quantize and
+ * gemm_mx_matmul give one after the other, and bit for bit the same where
+ * both ways take the same kernel (X and all scales laid out as the fast
+ * kernels take them); another kernel adds in another order.  Up to 16 rows, a decoding step's, are encoded
  * inside the product, in one launch, if X's rows are 16-byte aligned, Bt's
  * scale rows 4-byte aligned, every row stride below 2^26 bytes and N at most
  * 2^26 - 16; `workspace` may be NULL then.  Otherwise the codes go through it
@@ -122,7 +133,8 @@ int64_t gemm_mx_matmul_values_workspace_bytes(int64_t M, int64_t K);
  * feature.  dY is T x N of type y_dtype, dW F x N of type c_dtype (F32, F16,
  * BF16 each).  The codes enter the bfloat16 matrix instruction exactly; dY
  * does too: bfloat16 as it is, binary16 as the sum of two bfloat16 terms,
- * FP32 as the sum of three.  Accumulated in FP32, rounded once.  beta == 0:
+ * FP32 as the sum of three (bits below 2^-133, bfloat16's smallest step, are
+ * dropped).  Accumulated in FP32, rounded once.  beta == 0:
  * dW is not read.  T == 0: the empty sum.
  *
  * `workspace` (gemm_mx_wgrad_workspace_bytes bytes, 16-byte aligned, not
@@ -130,8 +142,9 @@ int64_t gemm_mx_matmul_values_workspace_bytes(int64_t M, int64_t K);
  * is not bfloat16 or N is no multiple of 8, and, where few outputs have many
  * tokens, the FP32 sums of S chunks of tokens, which are added in chunk
  * order.  The workspace may be NULL, or smaller than that: then a slower
- * kernel runs that needs none (as for a dY of rows that are not 16-byte
- * aligned though N is a multiple of 8, or scales off 4-byte words).
+ * kernel runs that needs none (as for a bfloat16 dY of rows that are not
+ * 16-byte aligned though N is a multiple of 8, or scales off 4-byte words):
+ * 8192 tokens, 4096 x 4096, rows of 4099: 1840 us against 201.
  */
 gemm_status_t gemm_mx_wgrad(int32_t y_dtype, int32_t c_dtype, int64_t T, int64_t F, int64_t N,
                             const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t lds,
