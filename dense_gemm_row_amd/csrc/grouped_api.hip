@@ -1,0 +1,89 @@
+// C-ABI entry points of the grouped products (include/gemm_grouped.h):
+// argument checks on the host, then the launch on the caller's stream.
+#include "api_checks.h"
+#include "grouped_internal.h"
+
+namespace gemm {
+namespace grouped {
+namespace {
+
+gemm_status_t check_types(int dtype, int c_dtype) {
+  if (!float_dtype(dtype)) return fail(GEMM_ERR_INVALID_ARG, "type %d is not F32, F16 or BF16", dtype);
+  if (c_dtype != dtype && c_dtype != GEMM_DTYPE_F32)
+    return fail(GEMM_ERR_INVALID_ARG, "the result's type %d is neither the operands' nor F32", c_dtype);
+  return GEMM_OK;
+}
+
+gemm_status_t check_sizes(int64_t G, int64_t T, int64_t K, int64_t N, const int32_t* offsets, Span* o) {
+  if (G < 0 || G > kMostGroups) return fail(GEMM_ERR_INVALID_ARG, "%lld groups: 0 to %lld", (long long)G, (long long)kMostGroups);
+  if (!size_ok(T) || !size_ok(K) || !size_ok(N)) return fail(GEMM_ERR_INVALID_ARG, "size below 0 or above 2^31-1");
+  if (!offsets) return fail(GEMM_ERR_INVALID_ARG, "offsets is NULL");
+  if ((uintptr_t)offsets % 4 != 0) return fail(GEMM_ERR_UNSUPPORTED, "offsets is not aligned to its elements");
+  *o = span(offsets, 1, 4 * (G + 1), 4 * (G + 1));
+  return GEMM_OK;
+}
+
+// G matrices of rows x cols, `stride` elements apart; `apart`: they must not
+// overlap (an output's).
+gemm_status_t check_stack(const char* name, const void* p, int64_t G, int64_t rows, int64_t cols, int64_t ld, int64_t stride,
+                          int64_t es, bool apart, Span* out) {
+  Span one;
+  if (stride < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative stride", name);
+  const gemm_status_t st = check_dense(name, p, G > 0 ? rows : 0, cols, ld, es, &one);
+  if (st != GEMM_OK) return st;
+  *out = one;
+  if (one.bytes == 0 || G <= 1) return GEMM_OK;
+  if (stride >= (int64_t)(kSpanLimit >> 3)) return fail(GEMM_ERR_INVALID_ARG, "%s: byte range reaches 2^63", name);
+  if (apart && (unsigned __int128)(uint64_t)stride * (unsigned)es < one.bytes)
+    return fail(GEMM_ERR_INVALID_ARG, "%s: the matrices of two groups overlap", name);
+  out->bytes += (unsigned __int128)(uint64_t)(G - 1) * (uint64_t)(stride * es);
+  if (out->bytes >= kSpanLimit) return fail(GEMM_ERR_INVALID_ARG, "%s: byte range reaches 2^63", name);
+  return GEMM_OK;
+}
+
+}  // namespace
+}  // namespace grouped
+}  // namespace gemm
+
+using namespace gemm;
+using namespace gemm::grouped;
+
+extern "C" {
+
+gemm_status_t gemm_grouped_matmul(int32_t dtype, int32_t c_dtype, int32_t trans_w, int64_t G, int64_t T, int64_t N, int64_t K,
+                                  const int32_t* offsets, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                  int64_t stride_w, void* Y, int64_t ldy, int32_t fill, void* stream) {
+  set_last_error(GEMM_OK, "");
+  gemm_status_t st = check_types(dtype, c_dtype);
+  if (st != GEMM_OK) return st;
+  if (trans_w != 0 && trans_w != 1) return fail(GEMM_ERR_INVALID_ARG, "trans_w is neither 0 nor 1");
+  if (fill != 0 && fill != 1) return fail(GEMM_ERR_INVALID_ARG, "fill is neither 0 nor 1");
+  Span o, x, w, y;
+  if ((st = check_sizes(G, T, K, N, offsets, &o)) != GEMM_OK) return st;
+  const int64_t es = dtype_bytes(dtype);
+  if ((st = check_dense("X", X, T, K, ldx, es, &x)) != GEMM_OK) return st;
+  if ((st = check_stack("W", W, G, trans_w ? N : K, trans_w ? K : N, ldw, stride_w, es, false, &w)) != GEMM_OK) return st;
+  if ((st = check_dense("Y", Y, T, N, ldy, dtype_bytes(c_dtype), &y)) != GEMM_OK) return st;
+  if (overlap(y, x) || overlap(y, w) || overlap(y, o)) return fail(GEMM_ERR_ALIAS, "Y overlaps an operand");
+  const MatmulArgs a{offsets, X, W, Y, ldx, ldw, stride_w, ldy, (int)G, (int)T, (int)N, (int)K, fill, trans_w};
+  return launched(launch_general(dtype, c_dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+gemm_status_t gemm_grouped_wgrad(int32_t dtype, int32_t c_dtype, int64_t G, int64_t T, int64_t K, int64_t N,
+                                 const int32_t* offsets, const void* X, int64_t ldx, const void* dY, int64_t ldy, void* dW,
+                                 int64_t ldw, int64_t stride_w, float alpha, float beta, void* stream) {
+  set_last_error(GEMM_OK, "");
+  gemm_status_t st = check_types(dtype, c_dtype);
+  if (st != GEMM_OK) return st;
+  Span o, x, y, w;
+  if ((st = check_sizes(G, T, K, N, offsets, &o)) != GEMM_OK) return st;
+  const int64_t es = dtype_bytes(dtype);
+  if ((st = check_dense("X", X, T, K, ldx, es, &x)) != GEMM_OK) return st;
+  if ((st = check_dense("dY", dY, T, N, ldy, es, &y)) != GEMM_OK) return st;
+  if ((st = check_stack("dW", dW, G, K, N, ldw, stride_w, dtype_bytes(c_dtype), true, &w)) != GEMM_OK) return st;
+  if (overlap(w, x) || overlap(w, y) || overlap(w, o)) return fail(GEMM_ERR_ALIAS, "dW overlaps an operand");
+  const WgradArgs a{offsets, X, dY, dW, ldx, ldy, ldw, stride_w, (int)G, (int)T, (int)K, (int)N, alpha, beta};
+  return launched(launch_general(dtype, c_dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,132 @@
+// Internal declarations of the grouped products (include/gemm_grouped.h):
+// kernel arguments, launch functions, and the search for a row tile's group.
+#pragma once
+
+#include "gemm_grouped.h"
+#include "gemm_internal.h"
+#include "grouped_bounds.h"
+
+namespace gemm {
+namespace grouped {
+
+constexpr int64_t kMostGroups = 65535;
+
+struct MatmulArgs {
+  const int32_t* offsets;
+  const void *X, *W;
+  void* Y;
+  int64_t ldx, ldw, stride_w, ldy;
+  int G, T, N, K;
+  int fill;
+  int trans_w;
+};
+
+struct WgradArgs {
+  const int32_t* offsets;
+  const void *X, *dY;
+  void* dW;
+  int64_t ldx, ldy, ldw, stride_w;
+  int G, T, K, N;
+  float alpha, beta;
+};
+
+// Any operands.
+hipError_t launch_general(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s);
+hipError_t launch_general(int dtype, int c_dtype, const WgradArgs& a, hipStream_t s);
+
+#if defined(__HIP__)
+// ---------------------------------------------------------------------------
+// Prefix sums and maxima over a wave's 64 lanes, six data-parallel moves each
+// (row shifts by 1, 2, 4 and 8, then the last lane of row 0 to row 1 and of
+// row 2 to row 3, and of row 1 to rows 2 and 3): about 100 cycles, where the
+// same through LDS permutes takes some 1500.  Values are not negative, so a
+// lane that a move does not reach gets 0, neutral for both.
+// ---------------------------------------------------------------------------
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int moved(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int scan_add(int x) {
+  x += moved<0x111, 0xf>(x);
+  x += moved<0x112, 0xf>(x);
+  x += moved<0x114, 0xf>(x);
+  x += moved<0x118, 0xf>(x);
+  x += moved<0x142, 0xa>(x);
+  x += moved<0x143, 0xc>(x);
+  return x;
+}
+__device__ __forceinline__ int larger(int a, int b) { return a > b ? a : b; }
+__device__ __forceinline__ int scan_max(int x) {
+  x = larger(x, moved<0x111, 0xf>(x));
+  x = larger(x, moved<0x112, 0xf>(x));
+  x = larger(x, moved<0x114, 0xf>(x));
+  x = larger(x, moved<0x118, 0xf>(x));
+  x = larger(x, moved<0x142, 0xa>(x));
+  x = larger(x, moved<0x143, 0xc>(x));
+  return x;
+}
+
+// What the lanes know of 64 consecutive segments: where lane l's, number
+// first + l, starts and ends, and the row tiles up to and with it.
+struct Segments {
+  int start, end, tiles;
+};
+// `end` and `tiles` of the segment before the first one come in and those of
+// the last one go out through `end0` and `tiles0`.
+__device__ __forceinline__ Segments segments(const int32_t* offsets, int G, int T, int fill, int bm, int first,
+                                             int& end0, int& tiles0) {
+  const int i = first + (int)(threadIdx.x & 63);
+  Segments s;
+  s.end = larger(scan_max(i <= G ? clamp_offset(offsets[i], T) : T), end0);
+  s.start = __builtin_amdgcn_update_dpp(end0, s.end, 0x138, 0xf, 0xf, false);  // (one lane up)
+  s.tiles = tiles0 + scan_add(segment_runs(i, G, fill) ? segment_tiles(s.end - s.start, bm) : 0);
+  end0 = __builtin_amdgcn_readlane(s.end, 63);
+  tiles0 = __builtin_amdgcn_readlane(s.tiles, 63);
+  return s;
+}
+
+// A row tile: rows row0 .. row0 + rows - 1 (rows <= bm) of group g, or
+// (g < 0) of no group.
+struct RowTile {
+  int g, row0, rows;
+};
+
+// Row tiles that the offsets give.  Every lane of the wave takes part.
+__device__ __forceinline__ int count_tiles(const int32_t* offsets, int G, int T, int fill, int bm) {
+  int end0 = 0, tiles0 = 0;
+  for (int first = 0; first < G + 2; first += 64) segments(offsets, G, T, fill, bm, first, end0, tiles0);
+  return tiles0;
+}
+
+// Row tile `rt` (below count_tiles) in the order of the rows.
+__device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int G, int T, int fill, int bm, int rt) {
+  int end0 = 0, tiles0 = 0;
+  for (int first = 0; first < G + 2; first += 64) {
+    const int before = tiles0;
+    const Segments s = segments(offsets, G, T, fill, bm, first, end0, tiles0);
+    if (rt >= tiles0) continue;
+    // The first lane whose running count passes rt; its own first tile is
+    // the count of the lane before it.
+    const int lane = (int)__builtin_ctzll(__ballot(s.tiles > rt));
+    const int below = lane == 0 ? before : __builtin_amdgcn_readlane(s.tiles, lane == 0 ? 0 : lane - 1);
+    const int start = __builtin_amdgcn_readlane(s.start, lane), end = __builtin_amdgcn_readlane(s.end, lane);
+    const int row0 = start + (rt - below) * bm, i = first + lane;
+    return {i > 0 && i <= G ? i - 1 : -1, row0, end - row0 < bm ? end - row0 : bm};
+  }
+  return {-1, 0, 0};
+}
+
+// Group g's rows [start, end).
+__device__ __forceinline__ void group_rows(const int32_t* offsets, int T, int g, int& start, int& end) {
+  int top = 0;
+  for (int first = 0; first <= g; first += 64) {
+    const int i = first + (int)(threadIdx.x & 63);
+    top = larger(top, __builtin_amdgcn_readlane(scan_max(i <= g ? clamp_offset(offsets[i], T) : 0), 63));
+  }
+  start = top;
+  end = larger(top, clamp_offset(__builtin_amdgcn_readfirstlane(offsets[g + 1]), T));
+}
+#endif
+
+}  // namespace grouped
+}  // namespace gemm
