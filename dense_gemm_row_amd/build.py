@@ -25,7 +25,8 @@ PROBE_LIB = os.path.join(HERE, "libgemm_probe.so")
 ARCH = "gfx950"
 
 SOURCES = ["gemm_api.hip", "splitk.hip", "sgemm_dl.hip", "sgemm_mfma.hip", "hgemm_mfma.hip", "hgemm_tr.hip", "sgemm_simt.hip",
-           "mx_api.hip", "mx_quant.hip", "mx_matmul.hip", "mx_wgrad.hip", "grouped_api.hip", "grouped_general.hip"]
+           "mx_api.hip", "mx_quant.hip", "mx_matmul.hip", "mx_wgrad.hip", "grouped_api.hip", "grouped_general.hip",
+           "w4_api.hip", "w4_quant.hip", "w4_matmul.hip"]
 # Sources compiled once for every set of definitions: their kernels are large
 # and the compiler's time grows faster than their number in a file (one 15 s,
 # two 39 s, four 115 s), so each object holds two (with and without the

@@ -25,7 +25,7 @@
  * Those of gemm_grouped.h, `offsets` among them.  Codes are 16-byte aligned,
  * ldq and stride_q multiples of 16 (else UNSUPPORTED).  Types of activations
  * and scales are GEMM_DTYPE_F16 or _BF16.  Errors besides: a group size that
- * is not 32, 64 or 128 -> INVALID_ARG.
+ * is not 32, 64 or 128, or K above 2^30 -> INVALID_ARG.
  */
 #ifndef DENSE_GEMM_ROW_AMD_GEMM_W4_H
 #define DENSE_GEMM_ROW_AMD_GEMM_W4_H
