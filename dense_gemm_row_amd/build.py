@@ -36,6 +36,8 @@ PARTS = {
     "mx_matmul_pipe.hip": [(f"{t}_{side}_{sc}", {"MX_DTYPE": d, "MX_SIDE": side, "MX_SC": sc})
                            for side in (256, 128) for sc in (16, 4) for t, d in _TYPES.items()],
     "mx_wgrad_pipe.hip": [(f"{t}_{side}", {"MX_DTYPE": d, "MX_SIDE": side}) for side in (256, 128) for t, d in _TYPES.items()],
+    "grouped_pipe.hip": [(f"{t}_{out}_{tile}", {"GROUPED_TYPE": _TYPES[t], "GROUPED_OUT": _TYPES[out], "GROUPED_TILE": tile})
+                         for tile in (256, 128, 32) for t in ("f16", "bf16") for out in (t, "f32")],
 }
 
 

@@ -41,6 +41,58 @@ gemm_status_t check_stack(const char* name, const void* p, int64_t G, int64_t ro
   return GEMM_OK;
 }
 
+// What the pipelined kernels take: 16-bit operands in whole 16-byte pieces,
+// a tile's and a slice's rows within 31 bits of bytes, and a grid within the
+// runtime's bounds.
+constexpr int64_t kFar = 1 << 20;
+constexpr int64_t kMostTiles = (1ll << 32) / 256 - 1;
+bool pieces(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && ld < kFar; }
+
+bool pipe_fits(int dtype, const MatmulArgs& a, int side) {
+  const int64_t tiles_n = ((int64_t)a.N + 127) / 128, tiles_m = most_tiles(a.T, a.G, a.fill, side);
+  return dtype != GEMM_DTYPE_F32 && a.K % 8 == 0 && (a.trans_w || a.N % 8 == 0) && pieces(a.X, a.ldx) && pieces(a.W, a.ldw) &&
+         (a.G <= 1 || a.stride_w % 8 == 0) && a.ldy < kFar && (tiles_m == 0 || tiles_n <= kMostTiles / tiles_m);
+}
+bool pipe_fits(int dtype, const WgradArgs& a) {
+  const int64_t tiles = (((int64_t)a.K + 127) / 128) * (((int64_t)a.N + 127) / 128);
+  return dtype != GEMM_DTYPE_F32 && a.K % 8 == 0 && a.N % 8 == 0 && pieces(a.X, a.ldx) && pieces(a.dY, a.ldy) && a.ldw < kFar &&
+         a.T < (1 << 30) && (a.G == 0 || tiles <= kMostTiles / a.G);
+}
+
+template <int DT, int CT>
+hipError_t on_tile(int side, const MatmulArgs& a, hipStream_t s) {
+  if (side == 32) return launch_pipe<DT, CT, 32>(a, s);
+  return side == 128 ? launch_pipe<DT, CT, 128>(a, s) : launch_pipe<DT, CT, 256>(a, s);
+}
+template <int DT, int CT>
+hipError_t on_tile(int side, const WgradArgs& a, hipStream_t s) {
+  return side == 128 ? launch_pipe<DT, CT, 128>(a, s) : launch_pipe<DT, CT, 256>(a, s);
+}
+template <class Args>
+hipError_t pipelined(int dtype, int c_dtype, int side, const Args& a, hipStream_t s) {
+  if (dtype == GEMM_DTYPE_BF16)
+    return c_dtype == GEMM_DTYPE_F32 ? on_tile<GEMM_DTYPE_BF16, GEMM_DTYPE_F32>(side, a, s)
+                                     : on_tile<GEMM_DTYPE_BF16, GEMM_DTYPE_BF16>(side, a, s);
+  return c_dtype == GEMM_DTYPE_F32 ? on_tile<GEMM_DTYPE_F16, GEMM_DTYPE_F32>(side, a, s)
+                                   : on_tile<GEMM_DTYPE_F16, GEMM_DTYPE_F16>(side, a, s);
+}
+
+int tile_for(const MatmulArgs& a) {
+  const int64_t rows = a.T / (a.G > 0 ? a.G : 1);
+  return rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+}
+int tile_for(const WgradArgs& a) {
+  return (int64_t)a.G * a.K * a.N >= 192ll * 256 * 256 ? 256 : 128;
+}
+
+hipError_t launch(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s) {
+  const int side = tile_for(a);
+  return pipe_fits(dtype, a, side) ? pipelined(dtype, c_dtype, side, a, s) : launch_general(dtype, c_dtype, a, s);
+}
+hipError_t launch(int dtype, int c_dtype, const WgradArgs& a, hipStream_t s) {
+  return pipe_fits(dtype, a) ? pipelined(dtype, c_dtype, tile_for(a), a, s) : launch_general(dtype, c_dtype, a, s);
+}
+
 }  // namespace
 }  // namespace grouped
 }  // namespace gemm
@@ -66,7 +118,7 @@ gemm_status_t gemm_grouped_matmul(int32_t dtype, int32_t c_dtype, int32_t trans_
   if ((st = check_dense("Y", Y, T, N, ldy, dtype_bytes(c_dtype), &y)) != GEMM_OK) return st;
   if (overlap(y, x) || overlap(y, w) || overlap(y, o)) return fail(GEMM_ERR_ALIAS, "Y overlaps an operand");
   const MatmulArgs a{offsets, X, W, Y, ldx, ldw, stride_w, ldy, (int)G, (int)T, (int)N, (int)K, fill, trans_w};
-  return launched(launch_general(dtype, c_dtype, a, static_cast<hipStream_t>(stream)));
+  return launched(grouped::launch(dtype, c_dtype, a, static_cast<hipStream_t>(stream)));
 }
 
 gemm_status_t gemm_grouped_wgrad(int32_t dtype, int32_t c_dtype, int64_t G, int64_t T, int64_t K, int64_t N,
@@ -83,7 +135,7 @@ gemm_status_t gemm_grouped_wgrad(int32_t dtype, int32_t c_dtype, int64_t G, int6
   if ((st = check_stack("dW", dW, G, K, N, ldw, stride_w, dtype_bytes(c_dtype), true, &w)) != GEMM_OK) return st;
   if (overlap(w, x) || overlap(w, y) || overlap(w, o)) return fail(GEMM_ERR_ALIAS, "dW overlaps an operand");
   const WgradArgs a{offsets, X, dY, dW, ldx, ldy, ldw, stride_w, (int)G, (int)T, (int)K, (int)N, alpha, beta};
-  return launched(launch_general(dtype, c_dtype, a, static_cast<hipStream_t>(stream)));
+  return launched(grouped::launch(dtype, c_dtype, a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

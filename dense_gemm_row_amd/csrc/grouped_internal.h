@@ -34,6 +34,14 @@ struct WgradArgs {
 hipError_t launch_general(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s);
 hipError_t launch_general(int dtype, int c_dtype, const WgradArgs& a, hipStream_t s);
 
+// 16-bit operands (DT) of whole 16-byte pieces, result of type CT, on tiles of
+// SIDE x SIDE (256, 128) or, the product alone, 32 x 256 (SIDE 32):
+// grouped_pipe.hip.
+template <int DT, int CT, int SIDE>
+hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s);
+template <int DT, int CT, int SIDE>
+hipError_t launch_pipe(const WgradArgs& a, hipStream_t s);
+
 #if defined(__HIP__)
 // ---------------------------------------------------------------------------
 // Prefix sums and maxima over a wave's 64 lanes, six data-parallel moves each
