@@ -85,6 +85,15 @@ MatmulArgs args_of(const gemm_w4_t* q, const void* X, int64_t ldx, void* Y, int6
           X, Y, ldx, ldy, (int)T, (int)N, (int)K, (int)G, offsets, fill};
 }
 
+template <int DT>
+hipError_t by_group(int group, const MatmulArgs& a, hipStream_t s) {
+  if (group == 32) return launch_few<DT, 32>(a, s);
+  return group == 64 ? launch_few<DT, 64>(a, s) : launch_few<DT, 128>(a, s);
+}
+hipError_t few_rows(int dtype, int group, const MatmulArgs& a, hipStream_t s) {
+  return dtype == GEMM_DTYPE_BF16 ? by_group<GEMM_DTYPE_BF16>(group, a, s) : by_group<GEMM_DTYPE_F16>(group, a, s);
+}
+
 hipError_t dequantize_all(int dtype, const gemm_w4_t* q, int64_t G, int64_t N, int64_t K, void* out, hipStream_t s) {
   const int64_t ld = row_values(K);
   const DequantArgs d{q->codes, q->scales, q->zeros, q->ldq, q->lds, q->ldz, out, ld, (int)N, (int)K,
@@ -160,7 +169,7 @@ gemm_status_t gemm_w4_matmul(int32_t dtype, int64_t M, int64_t N, int64_t K, con
   if ((st = check_workspace(workspace, workspace_bytes, need, c, x, y)) != GEMM_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!many_rows(M, 1, K))
-    return launched(launch_matmul(dtype, q->group, args_of(q, X, ldx, Y, ldy, M, N, K, 1, nullptr, 0), s));
+    return launched(few_rows(dtype, q->group, args_of(q, X, ldx, Y, ldy, M, N, K, 1, nullptr, 0), s));
   if ((st = launched(dequantize_all(dtype, q, 1, N, K, workspace, s))) != GEMM_OK) return st;
   return (dtype == GEMM_DTYPE_BF16 ? gemm_bf16_bt : gemm_f16_bt)(M, N, K, static_cast<const uint16_t*>(X), ldx,
                                                                  static_cast<const uint16_t*>(workspace), row_values(K),
@@ -198,7 +207,7 @@ gemm_status_t gemm_w4_grouped(int32_t dtype, int64_t G, int64_t T, int64_t N, in
   if ((st = check_workspace(workspace, workspace_bytes, need, c, x, y)) != GEMM_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!many_rows(T, G, K))
-    return launched(launch_matmul(dtype, q->group, args_of(q, X, ldx, Y, ldy, T, N, K, G, offsets, fill), s));
+    return launched(few_rows(dtype, q->group, args_of(q, X, ldx, Y, ldy, T, N, K, G, offsets, fill), s));
   if ((st = launched(dequantize_all(dtype, q, G, N, K, workspace, s))) != GEMM_OK) return st;
   return gemm_grouped_matmul(dtype, dtype, 1, G, T, N, K, offsets, X, ldx, workspace, row_values(K), N * row_values(K), Y, ldy,
                              fill, stream);

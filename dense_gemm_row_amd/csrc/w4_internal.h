@@ -50,7 +50,9 @@ struct MatmulArgs {
 
 hipError_t launch_quantize(int dtype, int s_dtype, bool trans, int group, const QuantArgs& a, hipStream_t s);
 hipError_t launch_dequantize(int dtype, int s_dtype, int group, int G, const DequantArgs& a, hipStream_t s);
-hipError_t launch_matmul(int dtype, int group, const MatmulArgs& a, hipStream_t s);
+// The products of few rows (w4_few.hip), activations of type DT, scales of GB k.
+template <int DT, int GB>
+hipError_t launch_few(const MatmulArgs& a, hipStream_t s);
 
 }  // namespace w4
 }  // namespace gemm

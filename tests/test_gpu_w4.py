@@ -5,11 +5,12 @@ values with their one rounding.  Products of inputs whose FP32 sums are all
 exact must be exact.  General ones must be within
 
     |Y - exact| <= (2 K + 4 ng + 24) 2^-23 S + half(type) |Y|,
-    S = sum |s| (q + z) |x|
+    S = sum |s| ((16 + q) + (16 + z)) |x|
 
-for few rows: of each term, K additions of q x and K of x (times z), then for
-each of ng groups two fused operations and an addition, 8 additions over the
-waves and the rest for the roundings themselves; half(type) as for the other
+for few rows (codes are multiplied as 16 + q, and 16 + z times the sum of x is
+taken off): of each term, K additions of (16 + q) x and K of x (times 16 + z),
+then for each of ng groups two fused operations and an addition, 8 additions
+over the waves and the rest for the roundings themselves; half(type) as for the other
 products.  With more rows the weights are rounded to the type first:
 
     ((K + 8) 2^-23 + half(type)) sum |w x| (1 + half(type)) + half(type) |Y|."""
@@ -228,6 +229,26 @@ def test_product(M, N, K, kind, group, zeros):
         assert bool((y._base == 7.0).all()), "wrote outside the result"
 
 
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("N, K, group", [(40, 128, 64), (33, 128, 32), (17, 384, 128), (50, 4224, 128), (16, 96, 32)])
+def test_scale_rows_longer_than_their_groups(N, K, group, kind, zeros):
+    """Rows of scales and zero points as `empty` lays them out, whole 256 k,
+    where the last has fewer: the bytes behind the groups hold anything."""
+    r = rng(6, N, K)
+    for M in (1, 20, 70):
+        q, value, _ = coded(r, (N, K), group, kind, zeros, -1, 2, whole=True)
+        own = w4.empty((N, K), group, "cuda", TYPES[kind], zeros)
+        own.scales._base.fill_(float("nan"))
+        own.scales.copy_(q.scales)
+        own.codes.copy_(q.codes)
+        if zeros:
+            own.zeros._base.fill_(GUARD)
+            own.zeros.copy_(q.zeros)
+        x, ex = dense(whole(r, (M, K)), kind)
+        assert torch.equal(w4.matmul(x, own).cpu(), torch.from_numpy(ex @ value.T).to(TYPES[kind]))
+
+
 EXPERTS = [
     (1, 1, 1, [0, 1]),
     (8, 128, 64, [0, 1, 2, 3, 4, 5, 6, 7, 8]),
@@ -399,7 +420,7 @@ def test_a_trained_layer_of_experts_served_in_4_bits(kind):
         check_codes(q[e], w[e].detach().t().double().cpu().numpy(), 64, kind)
     value = w4.dequantize(q, torch.float32).double().cpu().numpy()
     codes = np.stack([oracle.unpack(c, K) for c in q.codes.cpu().numpy()])
-    spread = np.repeat(q.scales.double().cpu().numpy(), 64, axis=2) * (codes + np.repeat(q.zeros.cpu().numpy(), 64, axis=2).astype(float))
+    spread = np.repeat(q.scales.double().cpu().numpy(), 64, axis=2) * (32.0 + codes + np.repeat(q.zeros.cpu().numpy(), 64, axis=2))
     x, ex = dense(r.standard_normal((6, K)), kind)
     offsets = [0, 1, 1, 4, 6]
     exact, mag = grouped_oracle.product(ex, value.transpose(0, 2, 1), offsets)

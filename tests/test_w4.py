@@ -196,7 +196,7 @@ def test_oracle_packs_and_decodes():
     assert packed.shape == (1, 32) and packed[0, 0] == 0x10 and packed[0, 19] == 0x76 and packed[0, 20] == 0
     assert np.array_equal(oracle.unpack(packed, 40), codes)
     v, size = oracle.values(codes, np.array([[2.0, 0.5]]), np.array([[8, 3]], np.uint8), 32)
-    assert v[0, 0] == -16 and v[0, 31] == 14 and v[0, 32] == -1.5 and size[0, 31] == 46 and size[0, 39] == 5
+    assert v[0, 0] == -16 and v[0, 31] == 14 and v[0, 32] == -1.5 and size[0, 31] == 110 and size[0, 39] == 21
 
 
 def test_oracle_quantises_by_hand():

@@ -64,8 +64,9 @@ def unpack(packed, K):
 
 
 def values(codes, scales, points, group):
-    """(values, s * (q + z): the size of what a product's sums go through)."""
+    """(values, s * (32 + q + z): the size of what a product's sums go through,
+    which add (16 + q) x and take off (16 + z) x)."""
     K = codes.shape[1]
     s = np.repeat(scales, group, axis=1)[:, :K]
     z = np.repeat(points.astype(np.float64), group, axis=1)[:, :K]
-    return s * (codes - z), np.abs(s) * (codes + z)
+    return s * (codes - z), np.abs(s) * (32 + codes + z)
