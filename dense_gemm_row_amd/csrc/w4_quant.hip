@@ -2,10 +2,10 @@
 //
 // A code is the whole number nearest to w / s.  The quotient in FP32 can fall
 // on a midpoint that the exact one only lies next to, so it is taken as a
-// guess (within one of the result) and decided by the exact products: with t
-// the guess, w - (t +- 1/2) s in one fused operation has the exact sign ((t +-
-// 1/2) s has at most 5 + 11 significant bits, and the one rounding keeps the
-// sign).
+// guess t, within one of the result, and decided by w - t s, which one fused
+// operation gives exactly: it is a multiple of w's last place and, as t is off
+// by at most 1/2 + 2^-18, no larger than w (t = 0: w itself).  Above s / 2, or
+// at it with t odd, the result is one further.
 #include "w4_internal.h"
 
 namespace gemm {
@@ -24,15 +24,14 @@ struct TypeOf<GEMM_DTYPE_F16> { typedef _Float16 type; };
 template <>
 struct TypeOf<GEMM_DTYPE_BF16> { typedef __bf16 type; };
 
-// The whole number nearest to w / s, ties to even, for s > 0; `inv` is about
-// 1 / s.  Beyond +-32 it is cut off (callers clamp to less).
-__device__ __forceinline__ float nearest(float w, float s, float inv) {
-  float t = __builtin_rintf(__builtin_fminf(__builtin_fmaxf(w * inv, -32.f), 32.f));
-  const float up = __builtin_fmaf(-(t + 0.5f), s, w), down = __builtin_fmaf(-(t - 0.5f), s, w);
-  const bool odd = ((int)t & 1) != 0;
-  if (up > 0.f || (up == 0.f && odd)) t += 1.f;
-  else if (down < 0.f || (down == 0.f && odd)) t -= 1.f;
-  return t;
+// The whole number nearest to w / s, ties to even, for s > 0; `inv` is 1 / s,
+// `half` s / 2 and `above` the next number up.  (Far beyond the codes, where a
+// scale is its type's largest, any number of w's sign: callers clamp.)
+__device__ __forceinline__ int nearest(float w, float s, float inv, float half, float above) {
+  const float t = __builtin_rintf(w * inv), d = __builtin_fmaf(-t, s, w);
+  const int i = (int)__builtin_fminf(__builtin_fmaxf(t, -64.f), 64.f);
+  const int one = (__builtin_bit_cast(int, d) >> 31) | 1;  // (d's sign)
+  return __builtin_fabsf(d) >= (i & 1 ? half : above) ? i + one : i;
 }
 
 // A group's scale (as its type's value) and zero point, from its least and
@@ -40,7 +39,8 @@ __device__ __forceinline__ float nearest(float w, float s, float inv) {
 template <class S>
 struct GroupScale {
   S s;
-  float value, up, inv, zero;  // (value * up and 1 / it are normal numbers)
+  float value, up, inv, half, above;  // (up: such that the others are normal numbers)
+  int zero;
   __device__ __forceinline__ GroupScale(float lo, float hi, bool finite, bool zeros) {
     const float most = sizeof(S) == 2 && (float)(S)65536.f != 65536.f ? 65504.f : 0x1.fep127f;
     float x;
@@ -56,18 +56,23 @@ struct GroupScale {
     // The reciprocal of a subnormal scale may be infinite: a small scale and
     // its values, at most some 15 such scales, are taken 2^64 times larger.
     up = value < 0x1p-60f ? 0x1p64f : 1.f;
-    inv = value > 0.f ? 1.f / (value * up) : 0.f;
-    zero = zeros ? 0.f : 8.f;
-    if (zeros && value > 0.f) zero = __builtin_fminf(__builtin_fmaxf(nearest(-lo * up, value * up, inv), 0.f), 15.f);
+    const float scaled = value * up;
+    inv = value > 0.f ? 1.f / scaled : 0.f;
+    // (A scale of 0: no value is past the half, all codes are the zero point.)
+    half = value > 0.f ? 0.5f * scaled : __builtin_inff();
+    above = value > 0.f ? __builtin_bit_cast(float, __builtin_bit_cast(unsigned, half) + 1) : __builtin_inff();
+    zero = zeros ? 0 : 8;
+    if (zeros && value > 0.f) zero = cut(nearest(-lo * up, scaled, inv, half, above));
     if (!finite) {
       s = (S)__builtin_nanf("");
-      value = 0.f;
-      zero = 0.f;
+      value = inv = 0.f;
+      half = above = __builtin_nanf("");  // (nothing compares with it)
+      zero = 0;
     }
   }
+  __device__ __forceinline__ static int cut(int i) { return i < 0 ? 0 : i > 15 ? 15 : i; }
   __device__ __forceinline__ unsigned code(float w) const {
-    if (!(value > 0.f)) return (unsigned)zero;
-    return (unsigned)__builtin_fminf(__builtin_fmaxf(nearest(w * up, value * up, inv) + zero, 0.f), 15.f);
+    return (unsigned)cut(nearest(w * up, value * up, inv, half, above) + zero);
   }
 };
 
@@ -119,49 +124,64 @@ __global__ void __launch_bounds__(THREADS) quantize_rows(QuantArgs p, int64_t pi
   }
 }
 
-// Down columns (X is K x N, the codes are its transpose's): a lane takes one
-// group of one column, so that a wave reads whole 64-column pieces of X's
-// rows; its GB / 2 code bytes are whole 16-byte pieces of its output row.
+// Down columns (X is K x N, the codes are its transpose's): a lane takes 32 k
+// of four columns, 16 lanes 64 columns, GB / 32 groups of 16 lanes a scale's k
+// (a wave 128).  So a wave reads whole 128-byte pieces of four rows of X at a
+// time (FP32: 256) and writes 64 bytes of a row of codes.  (4096 x 11008
+// bfloat16, groups of 128 with zero points: 35.6 us, 3.2 TB/s, bound by some 20
+// instructions a value; 112 us with a lane for a column's whole group.)
 template <class T, class S, int GB>
-__global__ void __launch_bounds__(THREADS) quantize_cols(QuantArgs p, int64_t blocks, int tiles_n) {
+__global__ void __launch_bounds__(THREADS) quantize_cols(QuantArgs p, int64_t blocks, int tiles_n, int vec) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const int64_t n = (int64_t)(b % tiles_n) * 64 + threadIdx.x % 64;
-    const int64_t j = b / tiles_n * (THREADS / 64) + threadIdx.x / 64, k0 = j * GB;
-    if (n >= p.N || k0 >= p.K) continue;
-    const int left = p.K - k0 < GB ? (int)(p.K - k0) : GB;
-    const T* x = static_cast<const T*>(p.X) + k0 * p.ldx + n;
-    T v[GB];
-    if (left == GB) {
+    const int64_t n0 = (b % tiles_n) * 64 + 4 * (l % 16);
+    const int64_t k0 = (b / tiles_n * (THREADS / 64) + wave) * 128 + 32 * (l / 16);
+    const int64_t left = p.K - k0, cols = p.N - n0;  // (0 or less: none)
+    const T* x = static_cast<const T*>(p.X) + k0 * p.ldx + n0;
+    T4 v[32];
+    if (vec && left >= 32 && cols >= 4) {
 #pragma unroll
-      for (int i = 0; i < GB; ++i) v[i] = x[i * p.ldx];
+      for (int i = 0; i < 32; ++i) v[i] = *reinterpret_cast<const T4*>(x + i * p.ldx);
     } else {
 #pragma unroll
-      for (int i = 0; i < GB; ++i) v[i] = i < left ? x[i * p.ldx] : (T)0.f;
-    }
-    float lo = 0.f, hi = 0.f;
-    bool finite = true;
+      for (int i = 0; i < 32; ++i)
 #pragma unroll
-    for (int i = 0; i < GB; ++i) {
-      lo = __builtin_fminf(lo, (float)v[i]);
-      hi = __builtin_fmaxf(hi, (float)v[i]);
-      finite = finite && is_finite(v[i]);
+        for (int c = 0; c < 4; ++c) v[i][c] = i < left && c < cols ? x[i * p.ldx + c] : (T)0.f;
     }
-    const GroupScale<S> g(lo, hi, finite, p.zeros != nullptr);
-    uint8_t* out = p.codes + n * p.ldq + k0 / 2;
 #pragma unroll
-    for (int c = 0; c < GB / 32; ++c) {
+    for (int c = 0; c < 4; ++c) {
+      float lo = 0.f, hi = 0.f, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float w = (float)v[i][c];
+        lo = __builtin_fminf(lo, w);
+        hi = __builtin_fmaxf(hi, w);
+        sum = __builtin_fmaf(w, 0.f, sum);  // (NaN where a value is infinite or NaN)
+      }
+#pragma unroll
+      for (int d = 16; d < GB / 2; d *= 2) {
+        lo = __builtin_fminf(lo, __shfl_xor(lo, d));
+        hi = __builtin_fmaxf(hi, __shfl_xor(hi, d));
+        sum += __shfl_xor(sum, d);
+      }
+      const GroupScale<S> g(lo, hi, sum == 0.f, p.zeros != nullptr);
+      if (left <= 0 || c >= cols) continue;
       uint4 w;
       unsigned* words = reinterpret_cast<unsigned*>(&w);
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         words[h] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) words[h] |= g.code((float)v[32 * c + 8 * h + i]) << (4 * i);
+        for (int i = 0; i < 8; ++i) words[h] |= g.code((float)v[8 * h + i][c]) << (4 * i);
       }
-      if (32 * c < left) *reinterpret_cast<uint4*>(out + 16 * c) = w;
+      const int64_t n = n0 + c;
+      *reinterpret_cast<uint4*>(p.codes + n * p.ldq + k0 / 2) = w;
+      if (k0 % GB == 0) {
+        static_cast<S*>(p.scales)[n * p.lds + k0 / GB] = g.s;
+        if (p.zeros) p.zeros[n * p.ldz + k0 / GB] = (uint8_t)g.zero;
+      }
     }
-    static_cast<S*>(p.scales)[n * p.lds + j] = g.s;
-    if (p.zeros) p.zeros[n * p.ldz + j] = (uint8_t)g.zero;
   }
 }
 
@@ -203,9 +223,10 @@ template <class T, class S, int GB>
 hipError_t quantize(bool trans, const QuantArgs& a, hipStream_t s) {
   if (trans) {
     const int64_t tiles_n = ((int64_t)a.N + 63) / 64;
-    const int64_t blocks = tiles_n * ((groups_of(a.K, GB) + THREADS / 64 - 1) / (THREADS / 64));
+    const int64_t blocks = tiles_n * (((int64_t)a.K + 2 * THREADS - 1) / (2 * THREADS));  // 128 k a wave
+    const int vec = (uintptr_t)a.X % (4 * sizeof(T)) == 0 && a.ldx % 4 == 0;
     hipLaunchKernelGGL((quantize_cols<T, S, GB>), dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(THREADS),
-                       0, s, a, blocks, (int)tiles_n);
+                       0, s, a, blocks, (int)tiles_n, vec);
   } else {
     const int per_row = (int)(groups_of(a.K, GB) * (GB / 8));
     const int vec = (uintptr_t)a.X % 16 == 0 && a.ldx * (int64_t)sizeof(T) % 16 == 0;
