@@ -45,7 +45,7 @@ gemm_status_t check_stack(const char* name, const void* p, int64_t G, int64_t ro
 // a tile's and a slice's rows within 31 bits of bytes, and a grid within the
 // runtime's bounds.
 constexpr int64_t kFar = 1 << 20;
-constexpr int64_t kMostTiles = (1ll << 32) / 256 - 1;
+constexpr int64_t kMostTiles = (1ll << 32) / 256 - 256;
 bool pieces(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && ld < kFar; }
 
 bool pipe_fits(int dtype, const MatmulArgs& a, int side) {
@@ -77,12 +77,37 @@ hipError_t pipelined(int dtype, int c_dtype, int side, const Args& a, hipStream_
                                    : on_tile<GEMM_DTYPE_F16, GEMM_DTYPE_F16>(side, a, s);
 }
 
-int tile_for(const MatmulArgs& a) {
-  const int64_t rows = a.T / (a.G > 0 ? a.G : 1);
-  return rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+// Time of `tiles` tiles, `at_once` of them at a time, half a round lost at the
+// end; `fixed` us a tile beside `per_slice` for each of its slices of 64 k.
+double tile_us(double tiles, int at_once, double tail, double fixed, double per_slice, double slices) {
+  const double rounds = tiles / at_once + tail;
+  return (rounds < 1. ? 1. : rounds) * (fixed + per_slice * slices);
 }
+
+// The tile of least time by a model of the measurements: 256 x 256, one
+// workgroup a CU, 1.35 us a slice and 13 beside; 128 x 128, two a CU, 1.1 us and
+// 5.5.  A group ends in half a tile on average.  (64 groups of 256 rows, K 1024,
+// N 2048: 128 x 128 130 us, 256 x 256 140; 8 groups of 256, 4096 x 4096: 139 and
+// 103; 32 groups of 128, 2048 x 1024: 47 and 60.)
+int tile_for(const MatmulArgs& a) {
+  const double slices = (a.K + 63) / 64, rows = a.T;
+  auto us = [&](int side, int at_once, double fixed, double per_slice) {
+    const double m = rows / side + 0.5 * (rows < a.G ? rows : a.G), n = (a.N + side - 1) / side;
+    return tile_us(m * n, at_once, 0.5, fixed, per_slice, slices);
+  };
+  return us(256, 256, 13., 1.35) < us(128, 512, 5.5, 1.1) ? 256 : 128;
+}
+// The gradient's likewise: a tile writes as many results however few rows its
+// group has, 20 us beside the slices on 256 x 256 and 8 on 128 x 128.  (8 groups
+// of 2048 rows, 4096 x 4096, FP32: 503 us and 574; 64 groups of 32 rows, 1024 x
+// 1024: 90 and 68; 8 of 512, 2048 x 2048: 73 and 65.)
 int tile_for(const WgradArgs& a) {
-  return (int64_t)a.G * a.K * a.N >= 192ll * 256 * 256 ? 256 : 128;
+  const double slices = (double)a.T / (a.G > 0 ? a.G : 1) / 64;
+  auto us = [&](int side, int at_once, double fixed, double per_slice) {
+    const double tiles = (double)a.G * ((a.K + side - 1) / side) * ((a.N + side - 1) / side);
+    return tile_us(tiles, at_once, 0., fixed, per_slice, slices < 2 ? 2 : slices);
+  };
+  return us(256, 256, 20., 1.35) < us(128, 512, 8., 1.1) ? 256 : 128;
 }
 
 hipError_t launch(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s) {

@@ -157,8 +157,9 @@ template <int DT, int CT, bool TRANS>
 __global__ void __launch_bounds__(THREADS) matmul_general(MatmulArgs p, int64_t tiles, int tiles_n, int vec_x, int vec_w) {
   typedef typename TypeOf<DT>::type T;
   typedef typename TypeOf<CT>::type C;
+  const RowTiles all(p.offsets, p.G, p.T, p.fill, TILE);
   for (int64_t b = blockIdx.x; b < tiles; b += gridDim.x) {
-    const RowTile t = find_tile(p.offsets, p.G, p.T, p.fill, TILE, (int)(b / tiles_n));
+    const RowTile t = all.find((int)(b / tiles_n));
     if (t.rows <= 0) return;  // (`tiles` are the most that offsets can give, in the order of the rows)
     const int n0 = (int)(b % tiles_n) * TILE, cols = p.N - n0 < TILE ? p.N - n0 : TILE;
     const T* X = static_cast<const T*>(p.X) + t.row0 * p.ldx;

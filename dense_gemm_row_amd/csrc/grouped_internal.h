@@ -99,30 +99,43 @@ struct RowTile {
   int g, row0, rows;
 };
 
-// Row tiles that the offsets give.  Every lane of the wave takes part.
-__device__ __forceinline__ int count_tiles(const int32_t* offsets, int G, int T, int fill, int bm) {
-  int end0 = 0, tiles0 = 0;
-  for (int first = 0; first < G + 2; first += 64) segments(offsets, G, T, fill, bm, first, end0, tiles0);
-  return tiles0;
+// The row tile `rt` in the order of the rows among segments `s`, whose first
+// one is `first` with `before` row tiles ahead; some lane's count passes rt.
+__device__ __forceinline__ RowTile tile_among(const Segments& s, int G, int bm, int first, int before, int rt) {
+  // The first lane whose running count passes rt; its own first tile is the
+  // count of the lane before it.
+  const int lane = (int)__builtin_ctzll(__ballot(s.tiles > rt));
+  const int below = lane == 0 ? before : __builtin_amdgcn_readlane(s.tiles, lane == 0 ? 0 : lane - 1);
+  const int start = __builtin_amdgcn_readlane(s.start, lane), end = __builtin_amdgcn_readlane(s.end, lane);
+  const int row0 = start + (rt - below) * bm, i = first + lane;
+  return {i > 0 && i <= G ? i - 1 : -1, row0, end - row0 < bm ? end - row0 : bm};
 }
 
-// Row tile `rt` (below count_tiles) in the order of the rows.
-__device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int G, int T, int fill, int bm, int rt) {
-  int end0 = 0, tiles0 = 0;
-  for (int first = 0; first < G + 2; first += 64) {
-    const int before = tiles0;
-    const Segments s = segments(offsets, G, T, fill, bm, first, end0, tiles0);
-    if (rt >= tiles0) continue;
-    // The first lane whose running count passes rt; its own first tile is
-    // the count of the lane before it.
-    const int lane = (int)__builtin_ctzll(__ballot(s.tiles > rt));
-    const int below = lane == 0 ? before : __builtin_amdgcn_readlane(s.tiles, lane == 0 ? 0 : lane - 1);
-    const int start = __builtin_amdgcn_readlane(s.start, lane), end = __builtin_amdgcn_readlane(s.end, lane);
-    const int row0 = start + (rt - below) * bm, i = first + lane;
-    return {i > 0 && i <= G ? i - 1 : -1, row0, end - row0 < bm ? end - row0 : bm};
+// All row tiles that offsets give: how many, and each by its number.  Every
+// lane of the wave takes part.  Up to 62 groups the offsets are read once.
+struct RowTiles {
+  const int32_t* offsets;
+  int G, T, fill, bm, count;
+  Segments first;
+  __device__ __forceinline__ RowTiles(const int32_t* offsets_, int G_, int T_, int fill_, int bm_)
+      : offsets(offsets_), G(G_), T(T_), fill(fill_), bm(bm_) {
+    int end = 0;
+    count = 0;
+    first = segments(offsets, G, T, fill, bm, 0, end, count);
+    for (int i = 64; i < G + 2; i += 64) segments(offsets, G, T, fill, bm, i, end, count);
   }
-  return {-1, 0, 0};
-}
+  // Tile rt, or (from count on) none, of 0 rows.
+  __device__ __forceinline__ RowTile find(int rt) const {
+    if (rt >= count) return {-1, 0, 0};
+    int end = __builtin_amdgcn_readlane(first.end, 63), tiles = __builtin_amdgcn_readlane(first.tiles, 63);
+    if (rt < tiles) return tile_among(first, G, bm, 0, 0, rt);
+    for (int i = 64;; i += 64) {
+      const int before = tiles;
+      const Segments s = segments(offsets, G, T, fill, bm, i, end, tiles);
+      if (rt < tiles) return tile_among(s, G, bm, i, before, rt);
+    }
+  }
+};
 
 // Group g's rows [start, end).
 __device__ __forceinline__ void group_rows(const int32_t* offsets, int T, int g, int& start, int& end) {

@@ -107,15 +107,21 @@ __device__ __forceinline__ void copy_one(const Copies<ACROSS, WIDTH, N>& o, int 
 #endif
 }
 
+// The LDS stages: arrays of their own, so that the compiler sees that copies
+// into one do not touch what is read from another.
+struct Stages {
+  uint8_t *a0, *b0, *a1, *b1;
+};
+
 // acc[j][i], register e of lane l: row 16i + l%16, column 16j + 4(l/16) + e of
 // the wave's share of A x B over K k; A has `rows` rows and B `cols` columns
 // from the tile on.
 template <bool BF, class S>
-__device__ __forceinline__ void tile_sums(const uint16_t* A, int lda, int rows, const uint16_t* B, int ldb, int cols, int K,
+__device__ __forceinline__ void tile_sums(const Stages& lds, const uint16_t* A, int lda, int rows, const uint16_t* B, int ldb, int cols, int K,
                                           f32x4 (&acc)[S::NB][S::MB]) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int MB = S::MB, NB = S::NB, BK = S::BK;
-  __shared__ __attribute__((aligned(1024))) uint8_t a0[S::A_STAGE], b0[S::B_STAGE], a1[S::A_STAGE], b1[S::B_STAGE];
+  uint8_t *const a0 = lds.a0, *const b0 = lds.b0, *const a1 = lds.a1, *const b1 = lds.b1;
   const int tid = threadIdx.x, l = tid & 63, r = l % 16, q = l / 16;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm0 = (wave / S::WAVES_N) * S::WM, wn0 = (wave % S::WAVES_N) * S::WN;
@@ -269,32 +275,67 @@ __device__ __forceinline__ void finish(void* C, int64_t ldc, int rows, int cols,
   else store<CT, S, false, EPI>(at, ldc, rows - wm0, cols - wn0, acc, alpha, beta);
 }
 
+// One tile of the product: its rows and columns on a workgroup of shape S.
 template <int DT, int CT, class S>
-__global__ void __launch_bounds__(64 * S::NW) matmul_pipe(MatmulArgs p, int tiles_n, int vec) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  // The grid holds the most tiles that offsets can give; those that there are
-  // are dealt to the XCDs in equal runs.
-  const int tiles_m = count_tiles(p.offsets, p.G, p.T, p.fill, S::BM);
-  if ((int64_t)blockIdx.x >= (int64_t)tiles_m * tiles_n) return;
-  int tm, tn;
-  tile_of_block(blockIdx.x, TileMap{tiles_m, tiles_n, GEMM_ORDER_XCD, 4, kXcds}, tm, tn);
-  const RowTile t = find_tile(p.offsets, p.G, p.T, p.fill, S::BM, tm);
-  // (Said to be uniform: the descriptors have to be in scalar registers.)
-  const int g = __builtin_amdgcn_readfirstlane(t.g), row0 = __builtin_amdgcn_readfirstlane(t.row0);
-  const int rows = __builtin_amdgcn_readfirstlane(t.rows), n0 = __builtin_amdgcn_readfirstlane(tn * S::BN);
+__device__ __forceinline__ void product_tile(const MatmulArgs& p, const Stages& lds, int g, int row0, int rows, int n0, int vec) {
   const uint16_t* X = static_cast<const uint16_t*>(p.X) + row0 * p.ldx;
   const uint16_t* W = static_cast<const uint16_t*>(p.W) + (g < 0 ? 0 : g) * p.stride_w + (S::B_ACROSS ? n0 : n0 * p.ldw);
   f32x4 acc[S::NB][S::MB];
   // (Rows of no group: a sum over no k.)
-  tile_sums<DT == GEMM_DTYPE_BF16, S>(X, (int)p.ldx, rows, W, (int)p.ldw, p.N - n0, g < 0 ? 0 : p.K, acc);
+  tile_sums<DT == GEMM_DTYPE_BF16, S>(lds, X, (int)p.ldx, rows, W, (int)p.ldw, p.N - n0, g < 0 ? 0 : p.K, acc);
   finish<CT, S, false>(static_cast<typename mx::TypeOf<CT>::type*>(p.Y) + row0 * p.ldy + n0, p.ldy, rows, p.N - n0, acc, vec, 1.f,
                        0.f);
+}
+
+// Tiles of 256 rows: those of no more than 128 rows, the last of most groups,
+// and the last tiles of the grid where they would occupy no more than half of
+// the CUs, each as two workgroups, run on 128 x 256 (HALF): about half the
+// time.  kCus workgroups fill the GPU, one a CU.
+constexpr int kCus = 256;
+
+template <int DT, int CT, class S, class HALF>
+__global__ void __launch_bounds__(64 * S::NW) matmul_pipe(MatmulArgs p, int tiles_n, int vec) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) uint8_t a0[S::A_STAGE], b0[S::B_STAGE], a1[S::A_STAGE], b1[S::B_STAGE];
+  const Stages lds{a0, b0, a1, b1};
+  constexpr bool HALVES = S::BM == 256;
+  // The grid holds the most tiles that offsets can give; those that there are
+  // are dealt to the XCDs in equal runs.
+  const RowTiles all(p.offsets, p.G, p.T, p.fill, S::BM);
+  const int tiles_m = all.count, tiles = tiles_m * tiles_n;
+  const int last = HALVES && tiles % kCus <= kCus / 2 ? tiles % kCus : 0, first = tiles - last;
+  int b = blockIdx.x, half = 0;
+  if (b >= first + 2 * last) return;
+  if (b < first) {
+    const int x = b % kXcds, q = first / kXcds, r = first % kXcds;  // (as tile_of_block)
+    b = x * q + (x < r ? x : r) + b / kXcds;
+  } else {
+    half = 1 + (b - first) % 2;
+    b = first + (b - first) / 2;
+  }
+  int tm, tn;
+  tile_of_block(b, TileMap{tiles_m, tiles_n, GEMM_ORDER_GROUPED, 4, kXcds}, tm, tn);
+  const RowTile t = all.find(tm);
+  // (Said to be uniform: the descriptors have to be in scalar registers.)
+  const int g = __builtin_amdgcn_readfirstlane(t.g), n0 = __builtin_amdgcn_readfirstlane(tn * S::BN);
+  int row0 = __builtin_amdgcn_readfirstlane(t.row0), rows = __builtin_amdgcn_readfirstlane(t.rows);
+  if constexpr (HALVES) {
+    if (half == 1) rows = rows < HALF::BM ? rows : HALF::BM;
+    if (half == 2) {
+      row0 += HALF::BM;
+      rows -= HALF::BM;
+      if (rows <= 0) return;
+    }
+    if (rows <= HALF::BM) return product_tile<DT, CT, HALF>(p, lds, g, row0, rows, n0, vec);
+  }
+  product_tile<DT, CT, S>(p, lds, g, row0, rows, n0, vec);
 #endif
 }
 
 template <int DT, int CT, class S, bool EPI>
 __global__ void __launch_bounds__(64 * S::NW) wgrad_pipe(WgradArgs p, int tiles_k, int tiles_n, int vec) {
 #if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) uint8_t a0[S::A_STAGE], b0[S::B_STAGE], a1[S::A_STAGE], b1[S::B_STAGE];
   // One group after another, each dealt to all XCDs: groups differ in rows.
   const int each = tiles_k * tiles_n;
   const int g = __builtin_amdgcn_readfirstlane((int)blockIdx.x / each);
@@ -308,7 +349,7 @@ __global__ void __launch_bounds__(64 * S::NW) wgrad_pipe(WgradArgs p, int tiles_
   const uint16_t* X = static_cast<const uint16_t*>(p.X) + first * p.ldx + m0;
   const uint16_t* dY = static_cast<const uint16_t*>(p.dY) + first * p.ldy + n0;
   f32x4 acc[S::NB][S::MB];
-  tile_sums<DT == GEMM_DTYPE_BF16, S>(X, (int)p.ldx, p.K - m0, dY, (int)p.ldy, p.N - n0, end - first, acc);
+  tile_sums<DT == GEMM_DTYPE_BF16, S>(Stages{a0, b0, a1, b1}, X, (int)p.ldx, p.K - m0, dY, (int)p.ldy, p.N - n0, end - first, acc);
   finish<CT, S, EPI>(static_cast<typename mx::TypeOf<CT>::type*>(p.dW) + g * p.stride_w + m0 * p.ldw + n0, p.ldw, p.K - m0,
                      p.N - n0, acc, vec, p.alpha, p.beta);
 #endif
@@ -328,12 +369,16 @@ template <int DT, int CT, int SIDE>
 hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s) {
   typedef TileOf<false, true, SIDE> S;
   typedef TileOf<false, false, SIDE> St;
+  typedef Tile<false, true, 128, 256, 64, 128> H;
+  typedef Tile<false, false, 128, 256, 64, 128> Ht;
   const int vec = rows_whole(a.Y, a.ldy, 0, a.N, CT == GEMM_DTYPE_F32 ? 4 : 2);
   const int64_t tiles_n = ((int64_t)a.N + S::BN - 1) / S::BN;
-  const dim3 grid((unsigned)(most_tiles(a.T, a.G, a.fill, S::BM) * tiles_n)), block(64 * S::NW);
-  if (grid.x == 0) return hipSuccess;
-  if (a.trans_w) hipLaunchKernelGGL((matmul_pipe<DT, CT, St>), grid, block, 0, s, a, (int)tiles_n, vec);
-  else hipLaunchKernelGGL((matmul_pipe<DT, CT, S>), grid, block, 0, s, a, (int)tiles_n, vec);
+  const int64_t tiles = most_tiles(a.T, a.G, a.fill, S::BM) * tiles_n;
+  if (tiles == 0) return hipSuccess;
+  // (Up to kCus / 2 tiles are two workgroups.)
+  const dim3 grid((unsigned)(tiles + (SIDE == 256 ? kCus / 2 : 0))), block(64 * S::NW);
+  if (a.trans_w) hipLaunchKernelGGL((matmul_pipe<DT, CT, St, Ht>), grid, block, 0, s, a, (int)tiles_n, vec);
+  else hipLaunchKernelGGL((matmul_pipe<DT, CT, S, H>), grid, block, 0, s, a, (int)tiles_n, vec);
   return hipGetLastError();
 }
 template hipError_t launch_pipe<GROUPED_TYPE, GROUPED_OUT, GROUPED_TILE>(const MatmulArgs&, hipStream_t);

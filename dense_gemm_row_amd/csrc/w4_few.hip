@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
   for (unsigned b = blockIdx.x; b < tiles; b += gridDim.x) {
     grouped::RowTile t;
     if (p.offsets) {
-      t = grouped::find_tile(p.offsets, p.G, p.T, p.fill, S::ROWS, (int)(b / tiles_n));
+      t = grouped::RowTiles(p.offsets, p.G, p.T, p.fill, S::ROWS).find((int)(b / tiles_n));
       if (t.rows <= 0) break;  // (the grid holds the most tiles that offsets can give)
     } else {
       t.g = 0;
