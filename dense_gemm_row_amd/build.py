@@ -25,7 +25,7 @@ PROBE_LIB = os.path.join(HERE, "libgemm_probe.so")
 ARCH = "gfx950"
 
 SOURCES = ["gemm_api.hip", "splitk.hip", "sgemm_dl.hip", "sgemm_mfma.hip", "hgemm_mfma.hip", "hgemm_tr.hip", "sgemm_simt.hip",
-           "mx_api.hip", "mx_quant.hip", "mx_matmul.hip", "mx_wgrad.hip", "grouped_api.hip", "grouped_general.hip",
+           "mx_api.hip", "mx_quant.hip", "mx_matmul.hip", "mx_wgrad.hip", "grouped_api.hip", "grouped_general.hip", "grouped_few.hip",
            "w4_api.hip", "w4_quant.hip"]
 # Sources compiled once for every set of definitions: their kernels are large
 # and the compiler's time grows faster than their number in a file (one 15 s,
@@ -37,7 +37,7 @@ PARTS = {
                            for side in (256, 128) for sc in (16, 4) for t, d in _TYPES.items()],
     "mx_wgrad_pipe.hip": [(f"{t}_{side}", {"MX_DTYPE": d, "MX_SIDE": side}) for side in (256, 128) for t, d in _TYPES.items()],
     "grouped_pipe.hip": [(f"{t}_{out}_{tile}", {"GROUPED_TYPE": _TYPES[t], "GROUPED_OUT": _TYPES[out], "GROUPED_TILE": tile})
-                         for tile in (256, 128, 32) for t in ("f16", "bf16") for out in (t, "f32")],
+                         for tile in (256, 128) for t in ("f16", "bf16") for out in (t, "f32")],
     "w4_few.hip": [(f"{t}_{group}", {"W4_TYPE": _TYPES[t], "W4_GROUP": group}) for t in ("f16", "bf16") for group in (32, 64, 128)],
 }
 

@@ -61,7 +61,6 @@ bool pipe_fits(int dtype, const WgradArgs& a) {
 
 template <int DT, int CT>
 hipError_t on_tile(int side, const MatmulArgs& a, hipStream_t s) {
-  if (side == 32) return launch_pipe<DT, CT, 32>(a, s);
   return side == 128 ? launch_pipe<DT, CT, 128>(a, s) : launch_pipe<DT, CT, 256>(a, s);
 }
 template <int DT, int CT>
@@ -85,17 +84,24 @@ double tile_us(double tiles, int at_once, double tail, double fixed, double per_
 }
 
 // The tile of least time by a model of the measurements: 256 x 256, one
-// workgroup a CU, 1.35 us a slice and 13 beside; 128 x 128, two a CU, 1.1 us and
-// 5.5.  A group ends in half a tile on average.  (64 groups of 256 rows, K 1024,
-// N 2048: 128 x 128 130 us, 256 x 256 140; 8 groups of 256, 4096 x 4096: 139 and
-// 103; 32 groups of 128, 2048 x 1024: 47 and 60.)
+// workgroup a CU, 1.35 us a slice and 13 beside; 128 x 128, two a CU, 1.1 us (0.9
+// one a CU) and 5.5; 16 x 64 (16), one a CU, 3 us and 0.2 a slice, and no faster
+// than 5.7 TB/s of the weights of each of its row tiles.  A group ends in half a
+// tile on average.  (64 groups of 256 rows, K 1024, N 2048: 128 x 128 130 us, 256
+// x 256 140; 8 groups of 256, 4096 x 4096: 139 and 103; 32 groups of 128, 2048 x
+// 1024: 47 and 60.  16 x 64 and 128 x 128: 32 groups of one row, 2048 x 1024, 18.6
+// and 31.6 us; of 8, 35 and 37; 64 groups of 16, 1024 x 2048, 85 and 64.)
 int tile_for(const MatmulArgs& a) {
-  const double slices = (a.K + 63) / 64, rows = a.T;
+  const double slices = (a.K + 63) / 64, rows = a.T, ends = 0.5 * (rows < a.G ? rows : a.G);
   auto us = [&](int side, int at_once, double fixed, double per_slice) {
-    const double m = rows / side + 0.5 * (rows < a.G ? rows : a.G), n = (a.N + side - 1) / side;
-    return tile_us(m * n, at_once, 0.5, fixed, per_slice, slices);
+    const double tiles = (rows / side + ends) * ((a.N + side - 1) / side);
+    return tile_us(tiles, at_once, 0.5, fixed, tiles < at_once / 2 ? 0.82 * per_slice : per_slice, slices);
   };
-  return us(256, 256, 13., 1.35) < us(128, 512, 5.5, 1.1) ? 256 : 128;
+  const double m = rows / 16 + ends, few = tile_us(m * ((a.N + 63) / 64), 256, 0., 3., 0.2, slices);
+  const double read = 2. * (m < rows ? m : rows) * a.N * a.K / 5.7e6, us16 = few > read ? few : read;
+  const double us128 = us(128, 512, 5.5, 1.1), us256 = us(256, 256, 13., 1.35);
+  if (us16 < us128 && us16 < us256) return 16;
+  return us256 < us128 ? 256 : 128;
 }
 // The gradient's likewise: a tile writes as many results however few rows its
 // group has, 20 us beside the slices on 256 x 256 and 8 on 128 x 128.  (8 groups
@@ -112,7 +118,8 @@ int tile_for(const WgradArgs& a) {
 
 hipError_t launch(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s) {
   const int side = tile_for(a);
-  return pipe_fits(dtype, a, side) ? pipelined(dtype, c_dtype, side, a, s) : launch_general(dtype, c_dtype, a, s);
+  if (!pipe_fits(dtype, a, side)) return launch_general(dtype, c_dtype, a, s);
+  return side == 16 ? launch_few(dtype, c_dtype, a, s) : pipelined(dtype, c_dtype, side, a, s);
 }
 hipError_t launch(int dtype, int c_dtype, const WgradArgs& a, hipStream_t s) {
   return pipe_fits(dtype, a) ? pipelined(dtype, c_dtype, tile_for(a), a, s) : launch_general(dtype, c_dtype, a, s);

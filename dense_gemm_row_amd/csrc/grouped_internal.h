@@ -35,12 +35,14 @@ hipError_t launch_general(int dtype, int c_dtype, const MatmulArgs& a, hipStream
 hipError_t launch_general(int dtype, int c_dtype, const WgradArgs& a, hipStream_t s);
 
 // 16-bit operands (DT) of whole 16-byte pieces, result of type CT, on tiles of
-// SIDE x SIDE (256, 128) or, the product alone, 32 x 256 (SIDE 32):
-// grouped_pipe.hip.
+// SIDE x SIDE (256, 128): grouped_pipe.hip.
 template <int DT, int CT, int SIDE>
 hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s);
 template <int DT, int CT, int SIDE>
 hipError_t launch_pipe(const WgradArgs& a, hipStream_t s);
+
+// The product on tiles of 16 rows x 64 columns, the same operands.
+hipError_t launch_few(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s);
 
 #if defined(__HIP__)
 // ---------------------------------------------------------------------------
@@ -111,8 +113,9 @@ __device__ __forceinline__ RowTile tile_among(const Segments& s, int G, int bm, 
   return {i > 0 && i <= G ? i - 1 : -1, row0, end - row0 < bm ? end - row0 : bm};
 }
 
-// All row tiles that offsets give: how many, and each by its number.  Every
-// lane of the wave takes part.  Up to 62 groups the offsets are read once.
+// All row tiles that offsets give (without offsets: one group of all rows): how
+// many, and each by its number.  Every lane of the wave takes part.  Up to 62
+// groups the offsets are read once.
 struct RowTiles {
   const int32_t* offsets;
   int G, T, fill, bm, count;
@@ -120,13 +123,15 @@ struct RowTiles {
   __device__ __forceinline__ RowTiles(const int32_t* offsets_, int G_, int T_, int fill_, int bm_)
       : offsets(offsets_), G(G_), T(T_), fill(fill_), bm(bm_) {
     int end = 0;
-    count = 0;
+    count = offsets ? 0 : segment_tiles(T, bm);
+    if (!offsets) return;
     first = segments(offsets, G, T, fill, bm, 0, end, count);
     for (int i = 64; i < G + 2; i += 64) segments(offsets, G, T, fill, bm, i, end, count);
   }
   // Tile rt, or (from count on) none, of 0 rows.
   __device__ __forceinline__ RowTile find(int rt) const {
     if (rt >= count) return {-1, 0, 0};
+    if (!offsets) return {0, rt * bm, T - rt * bm < bm ? T - rt * bm : bm};
     int end = __builtin_amdgcn_readlane(first.end, 63), tiles = __builtin_amdgcn_readlane(first.tiles, 63);
     if (rt < tiles) return tile_among(first, G, bm, 0, 0, rt);
     for (int i = 64;; i += 64) {

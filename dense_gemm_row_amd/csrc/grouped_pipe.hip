@@ -361,9 +361,8 @@ bool rows_whole(const void* C, int64_t ld, int64_t stride, int64_t cols, int64_t
 
 }  // namespace
 
-// Tiles of SIDE x SIDE, or (SIDE 32) of 32 x 256 for groups of few rows.
 template <bool A, bool B, int SIDE>
-using TileOf = Tile<A, B, SIDE, SIDE == 32 ? 256 : SIDE, SIDE == 32 ? 32 : SIDE / 2, SIDE == 32 ? 64 : SIDE / 2>;
+using TileOf = Tile<A, B, SIDE, SIDE, SIDE / 2, SIDE / 2>;
 
 template <int DT, int CT, int SIDE>
 hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s) {
@@ -383,7 +382,6 @@ hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s) {
 }
 template hipError_t launch_pipe<GROUPED_TYPE, GROUPED_OUT, GROUPED_TILE>(const MatmulArgs&, hipStream_t);
 
-#if GROUPED_TILE >= 128
 template <int DT, int CT, int SIDE>
 hipError_t launch_pipe(const WgradArgs& a, hipStream_t s) {
   typedef TileOf<true, true, SIDE> S;
@@ -398,7 +396,6 @@ hipError_t launch_pipe(const WgradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 template hipError_t launch_pipe<GROUPED_TYPE, GROUPED_OUT, GROUPED_TILE>(const WgradArgs&, hipStream_t);
-#endif
 
 }  // namespace grouped
 }  // namespace gemm

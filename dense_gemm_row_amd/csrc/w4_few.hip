@@ -389,8 +389,10 @@ hipError_t on_rows(const MatmulArgs& a, int kw, hipStream_t s) {
     if (kw == 8) return start<BF, Shape<GB, MB, 1, 8>, true>(a, s);
   }
   if (kw >= 4) return start<BF, Shape<GB, MB, 1, 4>, true>(a, s);
-  if (kw == 2) return start<BF, Shape<GB, MB, 1, 2>, true>(a, s);
-  return start<BF, Shape<GB, MB, 1, 1>, true>(a, s);
+  if constexpr (MB != 3) {  // (12 KB of X do not split over eight waves)
+    if (kw == 1) return start<BF, Shape<GB, MB, 1, 1>, true>(a, s);
+  }
+  return start<BF, Shape<GB, MB, 1, 2>, true>(a, s);
 }
 
 }  // namespace
@@ -413,9 +415,11 @@ hipError_t launch_few(const MatmulArgs& a, hipStream_t s) {
     return kw;
   };
   // More rows a tile read fewer codes and more of X at once (M 64: 4096 x 4096
-  // 14.1 us on 32 rows, 18.9 on 64; 4096 x 11008 30.2 and 24.7).
+  // 14.1 us on 32 rows, 18.9 on 64; 4096 x 11008 30.2 and 24.7.  M 33, 4096 x
+  // 11008: 21.8 us on 48 rows, 24.5 on 64).
   if (rows <= (a.offsets ? 16 : 32)) return on_rows<BF, GB, 1>(a, along_k(16), s);
   if (rows <= 32 || likely(64, 4) < 160) return on_rows<BF, GB, 2>(a, along_k(32), s);
+  if (rows <= 48 && !a.offsets) return on_rows<BF, GB, 3>(a, along_k(48), s);
   return on_rows<BF, GB, 4>(a, along_k(64), s);
 }
 
