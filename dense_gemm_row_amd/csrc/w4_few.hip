@@ -6,9 +6,13 @@
 //    along k, whose sums are added in order through LDS at the end, times NW
 //    along the columns.  A wave's codes are read straight into registers, 16
 //    rows of SPAN / 2 bytes; the waves of one part of k share X through LDS.
-//  * The codes of a group lie in a lane's load of group / 8 bytes: lane group q
-//    (of four) takes the q-th quarter of the group's k (any order common to
-//    both operands will do), a word of 8 codes for each matrix instruction.
+//  * A lane loads 16 bytes of codes, lane group q (of four) the q-th 32 k of 128,
+//    a word of 8 codes for each matrix instruction; any order of k common to
+//    both operands will do.  For groups shorter than 128 the lane groups
+//    exchange words, four instructions for four words, so that each matrix
+//    instruction has 32 k of one group.  (Loads of group / 8 bytes kept the cache
+//    busy with 16 rows each: 64 experts of 2048 x 2048, 512 rows, groups of 32, 111
+//    us.)
 //  * A code q goes to the top of a significand as 16 + q, exact in both types:
 //    four shifts and four mask-and-or for 8 codes.  (The conversions from E4M3,
 //    which reads a byte 0 .. 15 as that number times 2^-9, took a mask, two
@@ -65,6 +69,24 @@ __device__ __forceinline__ u32x4 widen(unsigned w) {
                  (w >> 2 & 0x03c003c0u) | 0x4c004c00u, (w >> 6 & 0x03c003c0u) | 0x4c004c00u};
 }
 
+// Word i of lane group q (16 lanes) becomes word q of lane group i.
+__device__ __forceinline__ void exchange(unsigned (&w)[4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  auto swap32 = [](unsigned& a, unsigned& b) __attribute__((always_inline)) {
+    const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(a, b, false, false));
+    a = t[0], b = t[1];
+  };
+  auto swap16 = [](unsigned& a, unsigned& b) __attribute__((always_inline)) {
+    const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a, b, false, false));
+    a = t[0], b = t[1];
+  };
+  swap32(w[0], w[2]);
+  swap32(w[1], w[3]);
+  swap16(w[0], w[1]);
+  swap16(w[2], w[3]);
+#endif
+}
+
 // Eight values in the same order.
 __device__ __forceinline__ u32x4 reorder(u32x4 x) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -81,7 +103,7 @@ template <int GB_, int MB_, int NB_, int KW_>
 struct Shape {
   static constexpr int GB = GB_, MB = MB_, NB = NB_, KW = KW_, NW = WAVES / KW_;
   static constexpr int SPAN = MB == 1 ? 256 : 128;
-  static constexpr int V = GB / 32;         // words of a lane's load, matrix instructions of a group
+  static constexpr int V = GB / 32;         // matrix instructions of a group
   static constexpr int GROUPS = SPAN / GB;  // groups of a span
   static constexpr int ROWS = 16 * MB, COLS = 16 * NB * NW;
   static constexpr bool SHARED = NW > 1;    // X goes through LDS
@@ -89,6 +111,13 @@ struct Shape {
   static constexpr int X_LDS = SHARED ? 2 * KW * X_BYTES : 0, SUMS = 4 * KW * ROWS * COLS;
   static constexpr int LDS = X_LDS > SUMS ? X_LDS : SUMS;
   static_assert(GROUPS >= 1 && XL >= 1 && XL * NW * 1024 == X_BYTES && LDS <= 160 * 1024, "shape");
+  // The 8 k (from the span's first on, over 8) of lane group q in the matrix
+  // instruction `step`: a lane's 16 bytes of codes are 32 k in a row, one such
+  // run after another in the steps of a group of 128; of shorter groups, the
+  // four lane groups have exchanged their words, so that a step is 32 k.
+  __host__ __device__ static constexpr int chunk(int step, int q) {
+    return GB == 128 ? 16 * (step / 4) + 4 * q + step % 4 : 4 * step + q;
+  }
   // 16-byte chunk c of row m of a span of X in LDS: 16 rows' reads of one
   // chunk fall on distinct banks.
   __device__ static constexpr int x_byte(int m, int c) { return 2 * SPAN * m + 16 * (c ^ (m % 16)); }
@@ -99,7 +128,7 @@ struct Shape {
 // [group][instruction][block]).
 template <class S>
 struct Codes {
-  unsigned w[S::NB][S::GROUPS][S::V], s[S::NB][(S::GROUPS + 1) / 2], z[S::NB][(S::GROUPS + 3) / 4];
+  unsigned w[S::NB][S::SPAN / 128][4], s[S::NB][(S::GROUPS + 1) / 2], z[S::NB][(S::GROUPS + 3) / 4];
   u32x4 x[S::XL];
 };
 
@@ -164,7 +193,7 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
     for (int j = 0; j < NB; ++j) {
       const int c = 16 * (NB * nw + j) + r;
       col[j] = c < cols ? c : cols - 1;
-      q_at[j] = c * (int)p.ldq + 4 * V * q;
+      q_at[j] = c * (int)p.ldq + 16 * q;
       s_at[j] = 2 * c * (int)p.lds;
       z_at[j] = c * (int)p.ldz;
     }
@@ -175,7 +204,7 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
     for (int i = 0; i < S::XL; ++i) {
       const int piece = 64 * (i * NW + nw) + l;
       const int m = S::SHARED ? piece / (SPAN / 8) : 16 * (i % MB) + r;
-      const int c = S::SHARED ? piece % (SPAN / 8) : GB / 8 * (i / MB / V) + V * q + i / MB % V;
+      const int c = S::SHARED ? piece % (SPAN / 8) : S::chunk(i / MB, q);
       row[i] = m < t.rows ? m : t.rows - 1;
       xk[i] = 8 * c;
       x_at[i] = 2 * (m * (int)p.ldx + 8 * c);
@@ -192,15 +221,18 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
           // (One uniform choice: past K an offset out of every range.)
           const unsigned q0 = k0 < K ? k0 / 2 : OOB, s0 = k0 < K ? 2 * (k0 / GB) : OOB, z0 = k0 < K ? k0 / GB : OOB;
 #pragma unroll
-          for (int h = 0; h < GROUPS; ++h) buffer_words<V>(from_q, q_at[j] + q0 + GB / 2 * h, c.w[j][h]);
+          for (int h = 0; h < SPAN / 128; ++h) buffer_words<4>(from_q, q_at[j] + q0 + 64 * h, c.w[j][h]);
           buffer_words<(GROUPS + 1) / 2, 2 * GROUPS>(from_s, s_at[j] + s0, c.s[j]);
           buffer_words<(GROUPS + 3) / 4, GROUPS>(from_z, z_at[j] + z0, c.z[j]);
         } else if (k0 < K) {
 #pragma unroll
-          for (int h = 0; h < GROUPS; ++h) {
-            int k = k0 + GB * h + 8 * V * q;  // (the lane's piece lies in whole 32 k, all of it there or none)
+          for (int h = 0; h < SPAN / 128; ++h) {
+            int k = k0 + 128 * h + 32 * q;  // (the lane's piece is a whole 32 k, all of it there or none)
             if (k >= padded) k = 0;
-            __builtin_memcpy(c.w[j][h], __builtin_assume_aligned(codes0 + col[j] * p.ldq + k / 2, 4 * V), 4 * V);
+            __builtin_memcpy(c.w[j][h], __builtin_assume_aligned(codes0 + col[j] * p.ldq + k / 2, 16), 16);
+          }
+#pragma unroll
+          for (int h = 0; h < GROUPS; ++h) {
             const int i = k0 / GB + h < ng ? k0 / GB + h : ng - 1;
             c.s[j][h / 2] = (h % 2 ? c.s[j][h / 2] : 0u) | (unsigned)scales0[col[j] * p.lds + i] << (16 * (h % 2));
             c.z[j][h / 4] = (h % 4 ? c.z[j][h / 4] : 0u) | (p.zeros ? (unsigned)zeros0[col[j] * p.ldz + i] : 0u) << (8 * (h % 4));
@@ -240,7 +272,13 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
 #pragma unroll
       for (int i = 0; i < MB; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     // A span's products; X from LDS or (not SHARED) from the lane's pieces.
-    auto multiply = [&](int k0, const Codes<S>& c, const uint8_t* xb) __attribute__((always_inline)) {
+    auto multiply = [&](int k0, Codes<S>& c, const uint8_t* xb) __attribute__((always_inline)) {
+      if constexpr (GB < 128) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int h = 0; h < SPAN / 128; ++h) exchange(c.w[j][h]);
+      }
 #pragma unroll
       for (int h = 0; h < GROUPS; ++h) {
         if (k0 / GB + h >= ng) break;
@@ -250,7 +288,7 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
 #pragma unroll
           for (int i = 0; i < MB; ++i)
             if constexpr (S::SHARED)
-              xo[v][i] = *reinterpret_cast<const h16x8_t*>(xb + S::x_byte(16 * i + r, GB / 8 * h + V * q + v));
+              xo[v][i] = *reinterpret_cast<const h16x8_t*>(xb + S::x_byte(16 * i + r, S::chunk(h * V + v, q)));
             else
               xo[v][i] = __builtin_bit_cast(h16x8_t, reorder(c.x[(h * V + v) * MB + i]));
         f32x4 part[NB][MB], sx[MB];
@@ -266,7 +304,7 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
           for (int i = 0; i < MB; ++i) sx[i] = mfma16<BF>(xo[v][i], ones, sx[i]);
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
-            const h16x8_t wv = __builtin_bit_cast(h16x8_t, widen<BF>(c.w[j][h][v]));
+            const h16x8_t wv = __builtin_bit_cast(h16x8_t, widen<BF>(c.w[j][(h * V + v) / 4][(h * V + v) % 4]));
 #pragma unroll
             for (int i = 0; i < MB; ++i) part[j][i] = mfma16<BF>(xo[v][i], wv, part[j][i]);
           }
