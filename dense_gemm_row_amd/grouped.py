@@ -56,15 +56,15 @@ def gemm_grouped_wgrad(dtype, c_dtype, G, T, K, N, offsets, X, ldx, dY, ldy, dW,
 # --------------------------------------------------------------------------
 # Torch forms (see mx.py for the launch stream and allocations).
 # --------------------------------------------------------------------------
-def _call(name, index, *args):
+def _call(L, name, index, *args):
     """The C-ABI call with the operands' device as the current one."""
-    fn = getattr(lib(), name)
-    if index == mx._torch.cuda.current_device():
-        status = fn(*args)
+    if index == mx._torch._C._cuda_getDevice():
+        status = getattr(L, name)(*args)
     else:
         with mx._torch.cuda.device(index):
-            status = fn(*args)
-    mx._check(status, name)
+            status = getattr(L, name)(*args)
+    if status != gemm.GEMM_OK:
+        raise gemm.GemmError(status, name)
 
 
 def _stack(w, name):
@@ -128,8 +128,8 @@ def matmul(x, w, offsets, transposed: bool = False, out=None, out_dtype=None, st
     c_dtype, _, _, ldy = mx._dense(out, "out")
     _result_dtype(out.dtype, x.dtype)
     mx._same_device(out, x)
-    _call("gemm_grouped_matmul", x.get_device(), dtype, c_dtype, 1 if transposed else 0, G, T, N, K, at, x.data_ptr(), ldx,
-          w.data_ptr(), ldw, stride_w, out.data_ptr(), ldy, 1 if fill else 0, on.handle)
+    _call(lib(), "gemm_grouped_matmul", x.get_device(), dtype, c_dtype, 1 if transposed else 0, G, T, N, K, at, x.data_ptr(),
+          ldx, w.data_ptr(), ldw, stride_w, out.data_ptr(), ldy, 1 if fill else 0, on.handle)
     return out
 
 
@@ -159,8 +159,8 @@ def weight_grad(x, dy, offsets, out=None, out_dtype=None, alpha: float = 1.0, be
     c_dtype, _, _, _, ldw, stride_w = _stack(out, "out")
     _result_dtype(out.dtype, x.dtype)
     mx._same_device(out, x)
-    _call("gemm_grouped_wgrad", x.get_device(), dtype, c_dtype, G, T, K, N, at, x.data_ptr(), ldx, dy.data_ptr(), ldy,
-          out.data_ptr(), ldw, stride_w, alpha, beta, on.handle)
+    _call(lib(), "gemm_grouped_wgrad", x.get_device(), dtype, c_dtype, G, T, K, N, at, x.data_ptr(), ldx, dy.data_ptr(),
+          ldy, out.data_ptr(), ldw, stride_w, alpha, beta, on.handle)
     return out
 
 

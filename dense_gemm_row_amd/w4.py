@@ -100,22 +100,26 @@ class W4Tensor:
             mx._load()
         torch = mx._torch
         cs, width, count = codes.shape, -(-cols // 32) * 16, -(-cols // group)
-        if len(cs) not in (2, 3) or codes.dtype != torch.uint8 or cs[-1] != width:
+        if len(cs) not in (2, 3) or codes.dtype is not torch.uint8 or cs[-1] != width:
             raise ValueError(f"codes must be uint8 with rows of {width} bytes for {cols} columns")
         if scales.dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("scales must be float16 or bfloat16")
-        if zeros is not None and zeros.dtype != torch.uint8:
-            raise TypeError("zeros must be uint8")
-        for t, n in ((scales, "scales"), (zeros, "zeros")):
-            if t is not None and tuple(t.shape) != (*cs[:-1], count):
-                raise ValueError(f"{n} must have shape {(*cs[:-1], count)}, not {tuple(t.shape)}")
-        for t in (codes, scales, zeros):
-            if t is None:
-                continue
-            if t.shape[-1] > 1 and t.stride(-1) != 1:
+        shape = (*cs[:-1], count)
+        if scales.shape != shape:
+            raise ValueError(f"scales must have shape {shape}, not {tuple(scales.shape)}")
+        if (width > 1 and codes.stride(-1) != 1) or (count > 1 and scales.stride(-1) != 1):
+            raise ValueError("rows must be contiguous (unit column stride)")
+        if scales.device != codes.device:
+            raise ValueError("codes and scales are on different devices")
+        if zeros is not None:
+            if zeros.dtype is not torch.uint8:
+                raise TypeError("zeros must be uint8")
+            if zeros.shape != shape:
+                raise ValueError(f"zeros must have shape {shape}, not {tuple(zeros.shape)}")
+            if count > 1 and zeros.stride(-1) != 1:
                 raise ValueError("rows must be contiguous (unit column stride)")
-            if t.device != codes.device:
-                raise ValueError("codes, scales and zeros are on different devices")
+            if zeros.device != codes.device:
+                raise ValueError("codes and zeros are on different devices")
         self.codes, self.scales, self.zeros, self.cols, self.group = codes, scales, zeros, cols, group
 
     @property
@@ -140,13 +144,16 @@ class W4Tensor:
     def _desc(self):
         """The C-ABI's description of these tensors."""
         c, s, z = self.codes, self.scales, self.zeros
+        cs, width, cd, sd = c.shape, s.shape[-1], c.stride(), s.stride()
         # (A single row's or matrix's stride means nothing.)
-        rows, apart = c.shape[-2] > 1, len(c.shape) == 3 and c.shape[0] > 1
-        width = s.shape[-1]
-        return GemmW4(c.data_ptr(), c.stride(-2) if rows else c.shape[-1], c.stride(0) if apart else 0,
-                      s.data_ptr(), s.stride(-2) if rows else width, s.stride(0) if apart else 0,
-                      None if z is None else z.data_ptr(), 0 if z is None else z.stride(-2) if rows else width,
-                      0 if z is None or not apart else z.stride(0), self.group)
+        rows, apart = cs[-2] > 1, len(cs) == 3 and cs[0] > 1
+        if z is None:
+            zp, zl, za = None, 0, 0
+        else:
+            zd = z.stride()
+            zp, zl, za = z.data_ptr(), zd[-2] if rows else width, zd[0] if apart else 0
+        return GemmW4(c.data_ptr(), cd[-2] if rows else cs[-1], cd[0] if apart else 0,
+                      s.data_ptr(), sd[-2] if rows else width, sd[0] if apart else 0, zp, zl, za, self.group)
 
     def __repr__(self) -> str:
         return f"W4Tensor({' x '.join(map(str, self.shape))}, groups of {self.group}, {self.device})"
@@ -161,17 +168,6 @@ def _coded(q, name, dims):
         raise ValueError(f"{name} must be " + ("one matrix (N x K)" if dims == 2 else "a stack of matrices (experts x N x K)"))
 
 
-def _call(name, index, *args):
-    """The C-ABI call with the operands' device as the current one."""
-    fn = getattr(lib(), name)
-    if index == mx._torch.cuda.current_device():
-        status = fn(*args)
-    else:
-        with mx._torch.cuda.device(index):
-            status = fn(*args)
-    mx._check(status, name)
-
-
 def empty(shape, group: int, device, scale_dtype=None, zeros: bool = True) -> W4Tensor:
     """Uninitialised 4-bit weights of shape (N, K) or (experts, N, K), scale
     rows of whole 256 k."""
@@ -181,11 +177,18 @@ def empty(shape, group: int, device, scale_dtype=None, zeros: bool = True) -> W4
     if group not in GROUPS:
         raise ValueError(f"groups of {group}: 32, 64 or 128")
     lead, K = tuple(shape[:-1]), shape[-1]
-    count, wide = -(-K // group), -(-K // 256) * (256 // group)
-    codes = torch.empty((*lead, -(-K // 32) * 16), dtype=torch.uint8, device=device)
-    scales = torch.empty((*lead, wide), dtype=scale_dtype or torch.bfloat16, device=device)[..., :count]
-    z = torch.empty((*lead, wide), dtype=torch.uint8, device=device)[..., :count] if zeros else None
-    return W4Tensor(codes, scales, z, K, group)
+    count = -(-K // group)
+    wide = -(-K // 256) * (256 // group)
+
+    def rows(n, dtype):
+        t = torch.empty((*lead, n), dtype=dtype, device=device)
+        return t if n == count else t[..., :count]
+    q = W4Tensor.__new__(W4Tensor)  # (as the checks of __init__ would have it)
+    q.codes = torch.empty((*lead, -(-K // 32) * 16), dtype=torch.uint8, device=device)
+    q.scales = rows(wide, scale_dtype or torch.bfloat16)
+    q.zeros = rows(wide, torch.uint8) if zeros else None
+    q.cols, q.group = K, group
+    return q
 
 
 def quantize(w, group: int = 128, zeros: bool = True, transposed: bool = False, scale_dtype=None, out: W4Tensor | None = None,
@@ -221,8 +224,8 @@ def quantize(w, group: int = 128, zeros: bool = True, transposed: bool = False, 
         on = mx._Launch(first, stream)
     for e in range(shape[0] if stack else 1):
         m, q = (w[e], out[e]) if stack else (w, out)
-        _call("gemm_w4_quantize", w.get_device(), dtype, mx._DTYPES[q.scales.dtype], 1 if transposed else 0, N, K, m.data_ptr(),
-              ldx, ctypes.byref(q._desc()), on.handle)
+        grouped._call(lib(), "gemm_w4_quantize", w.get_device(), dtype, mx._DTYPES[q.scales.dtype], 1 if transposed else 0, N, K,
+                      m.data_ptr(), ldx, ctypes.byref(q._desc()), on.handle)
     return out
 
 
@@ -243,8 +246,8 @@ def dequantize(q: W4Tensor, dtype=None, out=None, stream=None):
     for e in range(q.shape[0] if stack else 1):
         one, x = (q[e], out[e]) if stack else (q, out)
         x_dtype, N, K, ldx = mx._dense(x, "out")
-        _call("gemm_w4_dequantize", q.codes.get_device(), x_dtype, mx._DTYPES[q.scales.dtype], N, K, ctypes.byref(one._desc()),
-              x.data_ptr(), ldx, on.handle)
+        grouped._call(lib(), "gemm_w4_dequantize", q.codes.get_device(), x_dtype, mx._DTYPES[q.scales.dtype], N, K,
+                      ctypes.byref(one._desc()), x.data_ptr(), ldx, on.handle)
     return out
 
 
@@ -278,8 +281,8 @@ def matmul(x, q: W4Tensor, out=None, stream=None):
     dtype, M, K, ldx, N, on, out, ldy = _operands(x, q, 2, out, stream)
     need = 0 if M <= ROWS else lib().gemm_w4_matmul_workspace_bytes(M, N, K)
     ws = on.empty(need, mx._torch.uint8) if need > 0 else None
-    _call("gemm_w4_matmul", x.get_device(), dtype, M, N, K, x.data_ptr(), ldx, ctypes.byref(q._desc()), out.data_ptr(), ldy,
-          ws.data_ptr() if ws is not None else None, max(need, 0), on.handle)
+    grouped._call(lib(), "gemm_w4_matmul", x.get_device(), dtype, M, N, K, x.data_ptr(), ldx, ctypes.byref(q._desc()),
+                  out.data_ptr(), ldy, ws.data_ptr() if ws is not None else None, max(need, 0), on.handle)
     return out
 
 
@@ -295,6 +298,6 @@ def grouped_matmul(x, q: W4Tensor, offsets, out=None, stream=None):
     at = grouped._offsets(offsets, G, x)
     need = 0 if T <= ROWS * G else lib().gemm_w4_grouped_workspace_bytes(G, T, N, K)
     ws = on.empty(need, mx._torch.uint8) if need > 0 else None
-    _call("gemm_w4_grouped", x.get_device(), dtype, G, T, N, K, at, x.data_ptr(), ldx, ctypes.byref(q._desc()), out.data_ptr(),
-          ldy, 1 if fill else 0, ws.data_ptr() if ws is not None else None, max(need, 0), on.handle)
+    grouped._call(lib(), "gemm_w4_grouped", x.get_device(), dtype, G, T, N, K, at, x.data_ptr(), ldx, ctypes.byref(q._desc()),
+                  out.data_ptr(), ldy, 1 if fill else 0, ws.data_ptr() if ws is not None else None, max(need, 0), on.handle)
     return out
