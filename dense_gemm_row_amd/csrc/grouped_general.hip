@@ -16,6 +16,7 @@
 //    four consecutive columns of one row of the result.
 // Rows and columns past an operand's end are copies of others and not stored;
 // k past the end counts as zero.  64-bit addresses throughout.
+#include <type_traits>
 #include <utility>
 
 #include "grouped_internal.h"
@@ -346,13 +347,22 @@ hipError_t on_tile(const WgradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Whether tiles of 128 are likely to occupy the GPU.
-bool wide(const MatmulArgs& a) { return (a.T / 128 + (a.T < a.G ? a.T : a.G) / 2) * tiles_along(a.N, 128) >= 256; }
-bool wide(const WgradArgs& a) { return a.G * tiles_along(a.K, 128) * tiles_along(a.N, 128) >= 256; }
+// Tiles of 128 where groups fill them and enough are likely to occupy the GPU;
+// for FP32, bound by the matrix instruction, more of 64 are spread more evenly,
+// but the gradient's operands, down the rows both, take four reads each.  (16
+// bits, 8 groups of 1000 rows, 2001 x 2001: 160 us on 128 and 207 on 64, gradient
+// 173 and 226; 64 groups of 47 rows, 801 x 1203: 66 and 52; of 6, gradient 120
+// and 103.  FP32, 8 groups of 250 rows, 2048 x 2048: 272 and 203, gradient 204
+// and 220.)
+bool wide(const MatmulArgs& a) {
+  return a.T >= 96ll * a.G && (a.T / 128 + (a.T < a.G ? a.T : a.G) / 2) * tiles_along(a.N, 128) >= 256;
+}
+bool wide(const WgradArgs& a) { return a.T >= 64ll * a.G && a.G * tiles_along(a.K, 128) * tiles_along(a.N, 128) >= 256; }
 
 template <int DT, int CT, class Args>
 hipError_t launch(const Args& a, hipStream_t s) {
-  return wide(a) ? on_tile<DT, CT, 128>(a, s) : on_tile<DT, CT, 64>(a, s);
+  if constexpr (DT == GEMM_DTYPE_F32 && std::is_same_v<Args, MatmulArgs>) return on_tile<DT, CT, 64>(a, s);
+  else return wide(a) ? on_tile<DT, CT, 128>(a, s) : on_tile<DT, CT, 64>(a, s);
 }
 
 template <class Args>

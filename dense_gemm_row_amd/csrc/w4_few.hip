@@ -132,6 +132,10 @@ struct Codes {
   u32x4 x[S::XL];
 };
 
+// How a lane reads: ANY by element; SPANS, in 16-byte pieces wherever they
+// begin; WHOLE, aligned pieces through descriptors whose range ends them.
+enum Reads { ANY, SPANS, WHOLE };
+
 // N words (of BYTES bytes, 1 to 4 N) at an offset of a buffer.
 template <int N, int BYTES = 4 * N>
 __device__ __forceinline__ void buffer_words(__amdgpu_buffer_rsrc_t from, unsigned off, unsigned (&to)[N]) {
@@ -144,7 +148,25 @@ __device__ __forceinline__ void buffer_words(__amdgpu_buffer_rsrc_t from, unsign
 #endif
 }
 
-template <bool BF, class S, bool WHOLE>
+// BYTES bytes (1 to 4 N) wherever they begin.
+template <int BYTES, int N>
+__device__ __forceinline__ void words_at(const void* from, unsigned (&to)[N]) {
+  if constexpr (BYTES < 4) to[N - 1] = 0;
+  __builtin_memcpy(to, from, BYTES);
+}
+
+// The low end of a number of N words without its first n units of BITS bits,
+// zeros behind.
+template <int BITS, int N>
+__device__ __forceinline__ void without(unsigned (&w)[N], int n) {
+  typedef unsigned __int128 wide;
+  wide v = 0;
+  __builtin_memcpy(&v, w, 4 * N);
+  v = n * BITS < 128 ? v >> (n * BITS) : 0;
+  __builtin_memcpy(w, &v, 4 * N);
+}
+
+template <bool BF, class S, Reads HOW>
 __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned tiles, unsigned tiles_n) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef half_t<BF> T;
@@ -177,25 +199,27 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
     // results are not stored).
     const uint8_t* const codes0 = p.codes + g * p.stride_q + n0 * p.ldq;
     const uint16_t* const scales0 = static_cast<const uint16_t*>(p.scales) + g * p.stride_s + n0 * p.lds;
-    const uint8_t* const zeros0 = p.zeros ? p.zeros + g * p.stride_z + n0 * p.ldz : nullptr;
+    // (Without zero points some of the codes in their place, not used.)
+    const uint8_t* const zeros0 = p.zeros ? p.zeros + g * p.stride_z + n0 * p.ldz : codes0;
+    const int64_t ldz = p.zeros ? p.ldz : p.ldq;
     const uint16_t* const x0 = static_cast<const uint16_t*>(p.X) + t.row0 * p.ldx;
     auto uniform = [](const void* at, int64_t bytes) __attribute__((always_inline)) {
       return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(at), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
     };
-    const __amdgpu_buffer_rsrc_t from_q = uniform(codes0, WHOLE && K > 0 ? (cols - 1) * p.ldq + padded / 2 : 0);
-    const __amdgpu_buffer_rsrc_t from_s = uniform(scales0, WHOLE && K > 0 ? 2 * ((cols - 1) * p.lds + ng) : 0);
-    const __amdgpu_buffer_rsrc_t from_z = uniform(zeros0, WHOLE && K > 0 && p.zeros ? (cols - 1) * p.ldz + ng : 0);
-    const __amdgpu_buffer_rsrc_t from_x = uniform(x0, WHOLE && K > 0 ? 2 * ((t.rows - 1) * p.ldx + K) : 0);
-    const unsigned no_zeros = p.zeros ? 0u : 0x08080808u;
+    const __amdgpu_buffer_rsrc_t from_q = uniform(codes0, HOW == WHOLE && K > 0 ? (cols - 1) * p.ldq + padded / 2 : 0);
+    const __amdgpu_buffer_rsrc_t from_s = uniform(scales0, HOW == WHOLE && K > 0 ? 2 * ((cols - 1) * p.lds + ng) : 0);
+    const __amdgpu_buffer_rsrc_t from_z = uniform(zeros0, HOW == WHOLE && K > 0 && p.zeros ? (cols - 1) * p.ldz + ng : 0);
+    const __amdgpu_buffer_rsrc_t from_x = uniform(x0, HOW == WHOLE && K > 0 ? 2 * ((t.rows - 1) * p.ldx + K) : 0);
+    const unsigned kept = p.zeros ? ~0u : 0u, no_zeros = p.zeros ? 0u : 0x08080808u;
     int64_t col[NB];
     unsigned q_at[NB], s_at[NB], z_at[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int c = 16 * (NB * nw + j) + r;
-      col[j] = c < cols ? c : cols - 1;
-      q_at[j] = c * (int)p.ldq + 16 * q;
-      s_at[j] = 2 * c * (int)p.lds;
-      z_at[j] = c * (int)p.ldz;
+      col[j] = HOW == WHOLE || c < cols ? c : cols - 1;
+      q_at[j] = (unsigned)(col[j] * p.ldq) + (HOW == WHOLE ? 16 * q : 0);
+      s_at[j] = (unsigned)(2 * col[j] * p.lds);
+      z_at[j] = (unsigned)(col[j] * ldz);
     }
     // Piece i of X: its row, its k from the span's first on, its place in LDS.
     int row[S::XL], xk[S::XL], to[S::XL];
@@ -205,29 +229,40 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
       const int piece = 64 * (i * NW + nw) + l;
       const int m = S::SHARED ? piece / (SPAN / 8) : 16 * (i % MB) + r;
       const int c = S::SHARED ? piece % (SPAN / 8) : S::chunk(i / MB, q);
-      row[i] = m < t.rows ? m : t.rows - 1;
+      row[i] = HOW == WHOLE || m < t.rows ? m : t.rows - 1;
       xk[i] = 8 * c;
-      x_at[i] = 2 * (m * (int)p.ldx + 8 * c);
+      x_at[i] = 2 * (unsigned)(row[i] * (int)p.ldx) + (HOW == WHOLE ? 16 * c : 0);
       to[i] = S::x_byte(m, c);
     }
 
-    // The span at k0 (uniform; from K on, WHOLE reads nothing that counts).
-    // WHOLE has no branches: at one, the compiler would wait for loads that
-    // are on their way.
+    // The span at k0 (uniform; from K on, something that does not count).  WHOLE
+    // and SPANS have no branches: at one, the compiler would wait for loads that
+    // are on their way.  SPANS reads from before the end of a row what would
+    // lie past it, and moves it down (`trim`) where it is used.
     auto load = [&](int k0, Codes<S>& c) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        if constexpr (WHOLE) {
+        if constexpr (HOW == WHOLE) {
           // (One uniform choice: past K an offset out of every range.)
           const unsigned q0 = k0 < K ? k0 / 2 : OOB, s0 = k0 < K ? 2 * (k0 / GB) : OOB, z0 = k0 < K ? k0 / GB : OOB;
 #pragma unroll
           for (int h = 0; h < SPAN / 128; ++h) buffer_words<4>(from_q, q_at[j] + q0 + 64 * h, c.w[j][h]);
           buffer_words<(GROUPS + 1) / 2, 2 * GROUPS>(from_s, s_at[j] + s0, c.s[j]);
           buffer_words<(GROUPS + 3) / 4, GROUPS>(from_z, z_at[j] + z0, c.z[j]);
+        } else if constexpr (HOW == SPANS) {
+#pragma unroll
+          for (int h = 0; h < SPAN / 128; ++h) {
+            const int k = k0 + 128 * h + 32 * q;  // (the lane's piece is a whole 32 k, all of it there or none)
+            const unsigned off = q_at[j] + (unsigned)(k < padded ? k / 2 : 0);
+            __builtin_memcpy(c.w[j][h], __builtin_assume_aligned(codes0 + off, 16), 16);
+          }
+          const int i = k0 / GB < ng - GROUPS ? k0 / GB : ng - GROUPS;
+          words_at<2 * GROUPS>((const uint8_t*)scales0 + (s_at[j] + (unsigned)(2 * i)), c.s[j]);
+          words_at<GROUPS>(zeros0 + (z_at[j] + (unsigned)i), c.z[j]);
         } else if (k0 < K) {
 #pragma unroll
           for (int h = 0; h < SPAN / 128; ++h) {
-            int k = k0 + 128 * h + 32 * q;  // (the lane's piece is a whole 32 k, all of it there or none)
+            int k = k0 + 128 * h + 32 * q;
             if (k >= padded) k = 0;
             __builtin_memcpy(c.w[j][h], __builtin_assume_aligned(codes0 + col[j] * p.ldq + k / 2, 16), 16);
           }
@@ -243,15 +278,35 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
     auto load_x = [&](int k0, u32x4 (&xv)[S::XL]) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < S::XL; ++i) {
-        if constexpr (WHOLE) {
+        if constexpr (HOW == WHOLE) {
           const unsigned off = k0 + xk[i] < K ? x_at[i] + 2 * k0 : OOB;
           buffer_words<4>(from_x, off, reinterpret_cast<unsigned(&)[4]>(xv[i]));
+        } else if constexpr (HOW == SPANS) {
+          const int k = k0 + xk[i] < p.K - 8 ? k0 + xk[i] : p.K - 8;  // (K may be 0)
+          __builtin_memcpy(&xv[i], (const uint8_t*)x0 + (x_at[i] + (unsigned)(2 * k)), 16);
         } else {
           uint16_t e[8];
 #pragma unroll
           for (int u = 0; u < 8; ++u) e[u] = k0 + xk[i] + u < K ? x0[row[i] * p.ldx + k0 + xk[i] + u] : (uint16_t)0;
           __builtin_memcpy(&xv[i], e, 16);
         }
+      }
+    };
+    auto trim_x = [&](int k0, u32x4 (&xv)[S::XL]) __attribute__((always_inline)) {
+      if (HOW != SPANS || k0 + SPAN <= K) return;
+#pragma unroll
+      for (int i = 0; i < S::XL; ++i) {
+        const int past = k0 + xk[i] - (K - 8);
+        without<16>(reinterpret_cast<unsigned(&)[4]>(xv[i]), past > 0 ? past : 0);
+      }
+    };
+    auto trim_scales = [&](int k0, Codes<S>& c) __attribute__((always_inline)) {
+      const int past = k0 / GB - (ng - GROUPS);
+      if (HOW != SPANS || GROUPS == 1 || past <= 0) return;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        without<16>(c.s[j], past);
+        without<8>(c.z[j], past);
       }
     };
     auto store_x = [&](uint8_t* to_span, const u32x4 (&xv)[S::XL]) __attribute__((always_inline)) {
@@ -279,6 +334,8 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
 #pragma unroll
           for (int h = 0; h < SPAN / 128; ++h) exchange(c.w[j][h]);
       }
+      if constexpr (!S::SHARED) trim_x(k0, c.x);
+      trim_scales(k0, c);
 #pragma unroll
       for (int h = 0; h < GROUPS; ++h) {
         if (k0 / GB + h >= ng) break;
@@ -312,7 +369,7 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           const float s = widen16<BF>((unsigned short)(c.s[j][h / 2] >> (16 * (h % 2))));
-          const float z = -16.f - (float)((c.z[j][h / 4] | no_zeros) >> (8 * (h % 4)) & 255);
+          const float z = -16.f - (float)((c.z[j][h / 4] & kept | no_zeros) >> (8 * (h % 4)) & 255);
 #pragma unroll
           for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -322,8 +379,8 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
       }
     };
 
-    // Wave row kw takes spans kw, kw + KW, ..., each tile from another of them
-    // on (at one time the rows of all codes would be read at one offset, from
+    // Wave row kw takes spans kw, kw + KW, ..., each column of tiles from another
+    // of them on (at one time the rows of all codes would be read at one offset, from
     // few of the memory's channels); all that DEPTH spans need is on its way in
     // registers (loads return in order, so what is asked for late would hold up
     // what was asked for early).  SHARED X goes on into one of two places in
@@ -331,10 +388,11 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
     constexpr int DEPTH = S::SHARED ? 4 : 2;
     Codes<S> ring[DEPTH];
     const int spans = ((K + SPAN - 1) / SPAN + KW - 1) / KW;
-    const int turn = spans > 0 ? (int)(b % (unsigned)spans) : 0;
+    const int none = (K + SPAN - 1) / SPAN * SPAN;  // (a whole span past the end, so that a lane's 32 k are there or not)
+    const int turn = spans > 0 ? (int)(b % tiles_n % (unsigned)spans) : 0;
     auto at = [&](int i) __attribute__((always_inline)) {
       const int j = i + turn < spans ? i + turn : i + turn - spans;
-      return i < spans ? (kw + j * KW) * SPAN : K;
+      return i < spans ? (kw + j * KW) * SPAN : none;
     };
     // (In the order of the spans everywhere: the waits count on it.)
     auto fetch = [&](int i, Codes<S>& c) __attribute__((always_inline)) {
@@ -346,12 +404,14 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
     each<DEPTH>([&](auto D) __attribute__((always_inline)) { fetch(decltype(D)::value, ring[decltype(D)::value]); });
     if constexpr (S::SHARED) {
       barrier();  // (the tile before has been read)
+      trim_x(at(0), ring[0].x);
       store_x(xs, ring[0].x);
     }
     auto span = [&](int i, auto D) __attribute__((always_inline)) {
       constexpr int d = decltype(D)::value;
       if constexpr (S::SHARED) {
         barrier();  // this span's X has been written, the place of the next one's read
+        trim_x(at(i + 1), ring[(d + 1) % DEPTH].x);
         store_x(xs + (d + 1) % 2 * S::X_BYTES, ring[(d + 1) % DEPTH].x);
       }
       if (at(i) < K) multiply(at(i), ring[d], xs + d % 2 * S::X_BYTES);
@@ -392,17 +452,22 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
 #endif
 }
 
-// WHOLE: 16-byte pieces of X, a span's scales and zero points as one load each
-// (all of them there: a load that is partly past a descriptor's range gives
-// zeros), and a tile's rows and columns within 31 bits.
+// SPANS: there is a matrix, a row of which holds a whole span's scales and
+// eight k, and a tile's rows and columns are within 31 bits of bytes.  WHOLE: X
+// in aligned 16-byte pieces besides, a span's scales and zero points as one
+// aligned load each, all of them there (a load that is partly past a
+// descriptor's range gives zeros).  (4096 x 11008, groups of 64, 33 rows: 22.9 us
+// WHOLE, 25.5 as SPANS; 64 experts of 2048 x 2048, groups of 32, 512 rows: 60.8
+// and 69.4.  K 4095, one row of 4096 columns: 13.6 us SPANS, 29.3 by element.)
 template <class S>
-bool whole(const MatmulArgs& a) {
+Reads reads_of(const MatmulArgs& a) {
   constexpr int64_t g = S::GROUPS, far = 1 << 22;
-  return (uintptr_t)a.X % 16 == 0 && a.ldx % 8 == 0 && a.K % 8 == 0 && groups_of(a.K, S::GB) % g == 0 &&
-         (uintptr_t)a.scales % (2 * g) == 0 && a.lds % g == 0 &&
-         (a.G <= 1 || a.stride_s % g == 0) &&
-         (!a.zeros || ((uintptr_t)a.zeros % g == 0 && a.ldz % g == 0 && (a.G <= 1 || a.stride_z % g == 0))) && a.ldx < far &&
-         a.ldq < far && a.lds < far && a.ldz < far;
+  const int64_t ng = groups_of(a.K, S::GB);
+  if (a.G == 0 || a.K < 8 || ng < g || a.ldx >= far || a.ldq >= far || a.lds >= far || a.ldz >= far) return ANY;
+  const bool x = (uintptr_t)a.X % 16 == 0 && a.ldx % 8 == 0 && a.K % 8 == 0;
+  const bool s = (uintptr_t)a.scales % (2 * g) == 0 && a.lds % g == 0 && (a.G <= 1 || a.stride_s % g == 0);
+  const bool z = !a.zeros || ((uintptr_t)a.zeros % g == 0 && a.ldz % g == 0 && (a.G <= 1 || a.stride_z % g == 0));
+  return x && s && z && ng % g == 0 ? WHOLE : SPANS;
 }
 
 int64_t tiles_of(const MatmulArgs& a, int64_t rows, int64_t cols) {
@@ -410,27 +475,35 @@ int64_t tiles_of(const MatmulArgs& a, int64_t rows, int64_t cols) {
   return tiles_m * ((a.N + cols - 1) / cols);
 }
 
-template <bool BF, class S, bool WHOLE>
+template <bool BF, class S, Reads HOW>
 hipError_t start(const MatmulArgs& a, hipStream_t s) {
   const int64_t tiles = tiles_of(a, S::ROWS, S::COLS);
   if (tiles <= 0) return hipSuccess;
   if (tiles >= 1ll << 31) return hipErrorInvalidConfiguration;  // (of a result that no memory holds)
-  hipLaunchKernelGGL((matmul_few<BF, S, WHOLE>), dim3((unsigned)(tiles < kMostBlocks ? tiles : kMostBlocks)), dim3(64 * WAVES), 0,
+  hipLaunchKernelGGL((matmul_few<BF, S, HOW>), dim3((unsigned)(tiles < kMostBlocks ? tiles : kMostBlocks)), dim3(64 * WAVES), 0,
                      s, a, (unsigned)tiles, (unsigned)((a.N + S::COLS - 1) / S::COLS));
   return hipGetLastError();
 }
 
+template <bool BF, int GB, int MB, Reads HOW>
+hipError_t along(const MatmulArgs& a, int kw, hipStream_t s) {
+  if constexpr (MB == 1) {
+    if (kw == 8) return start<BF, Shape<GB, MB, 1, 8>, HOW>(a, s);
+  }
+  if (kw >= 4) return start<BF, Shape<GB, MB, 1, 4>, HOW>(a, s);
+  if constexpr (MB != 3) {  // (12 KB of X do not split over eight waves)
+    if (kw == 1) return start<BF, Shape<GB, MB, 1, 1>, HOW>(a, s);
+  }
+  return start<BF, Shape<GB, MB, 1, 2>, HOW>(a, s);
+}
+
 template <bool BF, int GB, int MB>
 hipError_t on_rows(const MatmulArgs& a, int kw, hipStream_t s) {
-  if (!whole<Shape<GB, MB, 1, 4>>(a)) return start<BF, Shape<GB, MB, 1, 4>, false>(a, s);
-  if constexpr (MB == 1) {
-    if (kw == 8) return start<BF, Shape<GB, MB, 1, 8>, true>(a, s);
+  switch (reads_of<Shape<GB, MB, 1, 4>>(a)) {
+    case WHOLE: return along<BF, GB, MB, WHOLE>(a, kw, s);
+    case SPANS: return along<BF, GB, MB, SPANS>(a, kw, s);
+    default: return start<BF, Shape<GB, 1, 1, 4>, ANY>(a, s);
   }
-  if (kw >= 4) return start<BF, Shape<GB, MB, 1, 4>, true>(a, s);
-  if constexpr (MB != 3) {  // (12 KB of X do not split over eight waves)
-    if (kw == 1) return start<BF, Shape<GB, MB, 1, 1>, true>(a, s);
-  }
-  return start<BF, Shape<GB, MB, 1, 2>, true>(a, s);
 }
 
 }  // namespace
