@@ -185,6 +185,8 @@ class _Launch:
 
     def empty(self, shape, dtype):
         if not self.other:
+            if type(shape) is tuple and len(shape) == 2:  # (`empty` takes 0.4 us longer to read its arguments)
+                return _torch.empty_strided(shape, (max(shape[1], 1), 1), dtype=dtype, device=self.device)
             return _torch.empty(shape, dtype=dtype, device=self.device)
         with _torch.cuda.stream(_torch.cuda.ExternalStream(self.handle, device=self.device)):
             return _torch.empty(shape, dtype=dtype, device=self.device)

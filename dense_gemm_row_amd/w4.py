@@ -110,7 +110,8 @@ class W4Tensor:
             raise ValueError(f"scales must have shape {shape}, not {tuple(scales.shape)}")
         if (width > 1 and codes.stride(-1) != 1) or (count > 1 and scales.stride(-1) != 1):
             raise ValueError("rows must be contiguous (unit column stride)")
-        if scales.device != codes.device:
+        at = codes.get_device()
+        if scales.get_device() != at:
             raise ValueError("codes and scales are on different devices")
         if zeros is not None:
             if zeros.dtype is not torch.uint8:
@@ -119,7 +120,7 @@ class W4Tensor:
                 raise ValueError(f"zeros must have shape {shape}, not {tuple(zeros.shape)}")
             if count > 1 and zeros.stride(-1) != 1:
                 raise ValueError("rows must be contiguous (unit column stride)")
-            if zeros.device != codes.device:
+            if zeros.get_device() != at:
                 raise ValueError("codes and zeros are on different devices")
         self.codes, self.scales, self.zeros, self.cols, self.group = codes, scales, zeros, cols, group
 
@@ -181,11 +182,16 @@ def empty(shape, group: int, device, scale_dtype=None, zeros: bool = True) -> W4
     count = -(-K // group)
     wide = -(-K // 256) * (256 // group)
 
+    def whole(n, dtype):
+        if len(lead) == 1:  # (`empty` takes 0.4 us longer to read its arguments)
+            return torch.empty_strided((lead[0], n), (max(n, 1), 1), dtype=dtype, device=device)
+        return torch.empty((*lead, n), dtype=dtype, device=device)
+
     def rows(n, dtype):
-        t = torch.empty((*lead, n), dtype=dtype, device=device)
+        t = whole(n, dtype)
         return t if n == count else t[..., :count]
     q = W4Tensor.__new__(W4Tensor)  # (as the checks of __init__ would have it)
-    q.codes = torch.empty((*lead, -(-K // 32) * 16), dtype=torch.uint8, device=device)
+    q.codes = whole(-(-K // 32) * 16, torch.uint8)
     q.scales = rows(wide, scale_dtype or torch.bfloat16)
     q.zeros = rows(wide, torch.uint8) if zeros else None
     q.cols, q.group = K, group
