@@ -84,23 +84,24 @@ double tile_us(double tiles, int at_once, double tail, double fixed, double per_
 }
 
 // The tile of least time by a model of the measurements: 256 x 256, one
-// workgroup a CU, 1.35 us a slice and 13 beside; 128 x 128, two a CU, 1.1 us (0.9
-// one a CU) and 5.5; 16 x 64 (16), one a CU, 3 us and 0.2 a slice, and no faster
-// than 5.7 TB/s of the weights of each of its row tiles.  A group ends in half a
-// tile on average.  (64 groups of 256 rows, K 1024, N 2048: 128 x 128 130 us, 256
-// x 256 140; 8 groups of 256, 4096 x 4096: 139 and 103; 32 groups of 128, 2048 x
-// 1024: 47 and 60.  16 x 64 and 128 x 128: 32 groups of one row, 2048 x 1024, 18.6
-// and 31.6 us; of 8, 35 and 37; 64 groups of 16, 1024 x 2048, 85 and 64.)
+// workgroup a CU, 1.35 us a slice and 13 beside; 128 x 128, two a CU, 1.1 us (0.66
+// one a CU) and 5.5, or with four stages (`alone`) 0.34 and 4.8; 16 x 64 (16),
+// one a CU, 0.2 us a slice and 3; none faster than 5.2 TB/s of the weights that
+// it reads, 16 x 64 those of each of its row tiles.  (64 groups of 256 rows, K
+// 1024, N 2048: 128 x 128 130 us, 256 x 256 140; 8 groups of 256, 4096 x 4096: 139
+// and 103; 32 groups of 128, 2048 x 1024: 47 and 60.  16 x 64 and 128 x 128: 32
+// groups of one row, 2048 x 1024, 18.6 and 31.6 us; 16 of 31, 1000 x 1000, 20.4 and
+// 12.0; 8 of 12, 4096 x 1024, 15.3 and 25.3; 64 of 16, 1024 x 2048, 85 and 64.)
 int tile_for(const MatmulArgs& a) {
-  const double slices = (a.K + 63) / 64, rows = a.T, ends = 0.5 * (rows < a.G ? rows : a.G);
-  auto us = [&](int side, int at_once, double fixed, double per_slice) {
-    const double tiles = (rows / side + ends) * ((a.N + side - 1) / side);
-    return tile_us(tiles, at_once, 0.5, fixed, tiles < at_once / 2 ? 0.82 * per_slice : per_slice, slices);
+  const double slices = (a.K + 63) / 64, groups = a.T < a.G ? a.T : a.G, of_one = 2. * a.N * a.K / 5.2e6, read = groups * of_one;
+  auto us = [&](int side, int at_once, double fixed, double per_slice, double lone) {
+    const double tiles = likely_tiles(a, side);
+    return tile_us(tiles, at_once, 0.5, fixed, tiles <= kCus ? lone : per_slice, slices);
   };
-  const double m = rows / 16 + ends, few = tile_us(m * ((a.N + 63) / 64), 256, 0., 3., 0.2, slices);
-  const double read = 2. * (m < rows ? m : rows) * a.N * a.K / 5.7e6, us16 = few > read ? few : read;
-  const double us128 = us(128, 512, 5.5, 1.1), us256 = us(256, 256, 13., 1.35);
-  if (us16 < us128 && us16 < us256) return 16;
+  const double m = a.T / 16. + 0.5 * groups, read16 = (m < a.T ? m : a.T) * of_one;
+  const double us16 = tile_us(m * ((a.N + 63) / 64), 256, 0.5, 3., 0.2, slices);
+  const double us128 = alone(a) ? 4.8 + 0.34 * slices : us(128, 512, 5.5, 1.1, 0.66), us256 = us(256, 256, 13., 1.35, 1.35);
+  if ((us16 > read16 ? us16 : read16) < (us128 > read ? us128 : read) && us16 < us256) return 16;
   return us256 < us128 ? 256 : 128;
 }
 // The gradient's likewise: a tile writes as many results however few rows its
@@ -110,7 +111,7 @@ int tile_for(const MatmulArgs& a) {
 int tile_for(const WgradArgs& a) {
   const double slices = (double)a.T / (a.G > 0 ? a.G : 1) / 64;
   auto us = [&](int side, int at_once, double fixed, double per_slice) {
-    const double tiles = (double)a.G * ((a.K + side - 1) / side) * ((a.N + side - 1) / side);
+    const double tiles = likely_tiles(a, side);
     return tile_us(tiles, at_once, 0., fixed, per_slice, slices < 2 ? 2 : slices);
   };
   return us(256, 256, 20., 1.35) < us(128, 512, 8., 1.1) ? 256 : 128;

@@ -41,6 +41,25 @@ hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s);
 template <int DT, int CT, int SIDE>
 hipError_t launch_pipe(const WgradArgs& a, hipStream_t s);
 
+// Tiles of `side` x `side` that are likely: a group ends in half a row tile on
+// average, and has one where it has a row.
+inline double likely_tiles(const MatmulArgs& a, int side) {
+  const double some = a.T < a.G ? a.T : a.G, m = (double)a.T / side + 0.5 * some;
+  return (m > some ? m : some) * ((a.N + side - 1) / side);
+}
+inline double likely_tiles(const WgradArgs& a, int side) {
+  return (double)a.G * ((a.K + side - 1) / side) * ((a.N + side - 1) / side);
+}
+// Whether the tiles of 128 x 128 do not have to share a CU (the product's with
+// some to spare: a second round costs more): then four LDS stages, three
+// slices ahead, hide what a second workgroup would.  (1000 rows, 8 groups, 2048 x
+// 2048: 17.5 us with four stages, 23.8 with two; 1024 rows, 32 groups, 1024 x 1024,
+// 256 tiles: 20.2 and 16.2.  Gradient of 16000 rows, 16 groups, 512 x 512: 31.9 and
+// 44.0; of 75 rows a group, 1024 x 1024: 7.9 and 7.4.)
+constexpr int kCus = 256;
+inline bool alone(const MatmulArgs& a) { return likely_tiles(a, 128) <= 240; }
+inline bool alone(const WgradArgs& a) { return likely_tiles(a, 128) <= kCus && a.T >= 384ll * a.G; }
+
 // The product on tiles of 16 rows x 64 columns, the same operands.
 hipError_t launch_few(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s);
 

@@ -40,10 +40,10 @@ __device__ __forceinline__ void mfma_asm(f32x4& c, i32x4 a, i32x4 b) {
 // past an operand's end are past their descriptor's range, or masked, and land
 // in LDS as zeros: the last rows of a group's tile, the end of k, and for the
 // gradient the end of the group's rows.
-template <bool A_ACROSS_, bool B_ACROSS_, int BM_, int BN_, int WM_, int WN_>
+template <bool A_ACROSS_, bool B_ACROSS_, int BM_, int BN_, int WM_, int WN_, int NS_ = 2>
 struct Tile {
   static constexpr bool A_ACROSS = A_ACROSS_, B_ACROSS = B_ACROSS_;
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = 64;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = 64, NS = NS_;
   static constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N;
   static constexpr int MB = WM / 16, NB = WN / 16, NMMA = MB * NB;
   static constexpr int A_STAGE = BM * 2 * BK, B_STAGE = BN * 2 * BK;
@@ -107,21 +107,31 @@ __device__ __forceinline__ void copy_one(const Copies<ACROSS, WIDTH, N>& o, int 
 #endif
 }
 
-// The LDS stages: arrays of their own, so that the compiler sees that copies
-// into one do not touch what is read from another.
+// The LDS stages, A and behind it B: arrays of their own, so that the compiler
+// sees that copies into one do not touch what is read from another.
+template <int NS>
 struct Stages {
-  uint8_t *a0, *b0, *a1, *b1;
+  uint8_t* at[NS];
 };
+
+// mx::loop_barrier, but for the last N copies, which need not have landed.
+template <int N>
+__device__ __forceinline__ void barrier_but() {
+  static_assert(N < 64, "what the wait can count");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);  // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // acc[j][i], register e of lane l: row 16i + l%16, column 16j + 4(l/16) + e of
 // the wave's share of A x B over K k; A has `rows` rows and B `cols` columns
 // from the tile on.
 template <bool BF, class S>
-__device__ __forceinline__ void tile_sums(const Stages& lds, const uint16_t* A, int lda, int rows, const uint16_t* B, int ldb, int cols, int K,
+__device__ __forceinline__ void tile_sums(const Stages<S::NS>& lds, const uint16_t* A, int lda, int rows, const uint16_t* B, int ldb, int cols, int K,
                                           f32x4 (&acc)[S::NB][S::MB]) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int MB = S::MB, NB = S::NB, BK = S::BK;
-  uint8_t *const a0 = lds.a0, *const b0 = lds.b0, *const a1 = lds.a1, *const b1 = lds.b1;
+  constexpr int MB = S::MB, NB = S::NB, BK = S::BK, NS = S::NS;
   const int tid = threadIdx.x, l = tid & 63, r = l % 16, q = l / 16;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm0 = (wave / S::WAVES_N) * S::WM, wn0 = (wave % S::WAVES_N) * S::WN;
@@ -199,29 +209,41 @@ __device__ __forceinline__ void tile_sums(const Stages& lds, const uint16_t* A, 
   };
   // The slice at k0 in stage c: step 0 with step 1's reads; the next slice
   // has landed and every wave has read stage c; step 1 with the next stage's
-  // reads and the copies of the slice after next into stage c.
+  // reads and the copies of the slice NS further into stage c.
   auto slice = [&](auto C, int k0) __attribute__((always_inline)) {
     constexpr int c = decltype(C)::value;
-    uint8_t *la = c ? a1 : a0, *lb = c ? b1 : b0, *na = c ? a0 : a1, *nb = c ? b0 : b1;
+    uint8_t *la = lds.at[c], *lb = la + S::A_STAGE, *na = lds.at[(c + 1) % NS], *nb = na + S::A_STAGE;
     step(IC<0>{}, [&](auto F) __attribute__((always_inline)) { read(la, lb, IC<1>{}, F); }, [](auto) {});
-    const int next = k0 + 2 * BK;
+    const int next = k0 + NS * BK;
     const __amdgpu_buffer_rsrc_t ra = range_a(next), rb = range_b(next);
-    mx::loop_barrier();
+    barrier_but<(NS - 2) * S::LPS>();
     __builtin_amdgcn_sched_barrier(0);
     step(IC<1>{}, [&](auto F) __attribute__((always_inline)) { read(na, nb, IC<0>{}, F); },
          [&](auto Q) __attribute__((always_inline)) { copy(ra, rb, K - next, la, lb, Q); });
   };
   // (With no k at all the stages get zeros and the loop is not entered.)
-  const __amdgpu_buffer_rsrc_t ra0 = range_a(0), rb0 = range_b(0), ra1 = range_a(BK), rb1 = range_b(BK);
-  mx::static_for([&](auto Q) __attribute__((always_inline)) {
-    copy(ra0, rb0, K, a0, b0, Q);
-    copy(ra1, rb1, K - BK, a1, b1, Q);
-  }, std::make_integer_sequence<int, S::LPS>{});
-  mx::loop_barrier();
-  mx::static_for([&](auto F) __attribute__((always_inline)) { read(a0, b0, IC<0>{}, F); },
+  mx::static_for([&](auto N) __attribute__((always_inline)) {
+    constexpr int n = decltype(N)::value;
+    const __amdgpu_buffer_rsrc_t ra = range_a(n * BK), rb = range_b(n * BK);
+    mx::static_for([&](auto Q) __attribute__((always_inline)) { copy(ra, rb, K - n * BK, lds.at[n], lds.at[n] + S::A_STAGE, Q); },
+                   std::make_integer_sequence<int, S::LPS>{});
+  }, std::make_integer_sequence<int, NS>{});
+  barrier_but<(NS - 1) * S::LPS>();
+  mx::static_for([&](auto F) __attribute__((always_inline)) { read(lds.at[0], lds.at[0] + S::A_STAGE, IC<0>{}, F); },
                  std::make_integer_sequence<int, MB + NB>{});
   mx::mfma_guard();
-  for (int64_t k0 = 0; k0 < K; k0 += 2 * BK) {
+  // (Slices past the end are zeros.  No way out of the loop's middle: at its
+  // start the compiler would wait for copies that are on their way.)
+  int64_t k0 = 0;
+  if constexpr (NS == 4) {
+    for (; k0 + 2 * BK < K; k0 += NS * BK) {
+      slice(IC<0>{}, (int)k0);
+      slice(IC<1>{}, (int)k0 + BK);
+      slice(IC<2>{}, (int)k0 + 2 * BK);
+      slice(IC<3>{}, (int)k0 + 3 * BK);
+    }
+  }
+  for (; k0 < K; k0 += 2 * BK) {
     slice(IC<0>{}, (int)k0);
     slice(IC<1>{}, (int)k0 + BK);
   }
@@ -296,9 +318,16 @@ __device__ __forceinline__ void finish(void* C, int64_t ldc, int rows, int cols,
   else store<CT, S, false, EPI>(at, ldc, rows - wm0, cols - wn0, acc, alpha, beta);
 }
 
+#define LDS_STAGES(S, lds) \
+  constexpr int kStage = S::A_STAGE + S::B_STAGE, kMore = S::NS > 2 ? kStage : 16; \
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage], s1[kStage], s2[kMore], s3[kMore]; \
+  Stages<S::NS> lds; \
+  if constexpr (S::NS > 2) lds = {{s0, s1, s2, s3}}; \
+  else lds = {{s0, s1}};
+
 // One tile of the product: its rows and columns on a workgroup of shape S.
 template <int DT, int CT, class S>
-__device__ __forceinline__ void product_tile(const MatmulArgs& p, const Stages& lds, int g, int row0, int rows, int n0, int vec) {
+__device__ __forceinline__ void product_tile(const MatmulArgs& p, const Stages<S::NS>& lds, int g, int row0, int rows, int n0, int vec) {
   const uint16_t* X = static_cast<const uint16_t*>(p.X) + row0 * p.ldx;
   const uint16_t* W = static_cast<const uint16_t*>(p.W) + (g < 0 ? 0 : g) * p.stride_w + (S::B_ACROSS ? n0 : n0 * p.ldw);
   f32x4 acc[S::NB][S::MB];
@@ -312,13 +341,11 @@ __device__ __forceinline__ void product_tile(const MatmulArgs& p, const Stages& 
 // and the last tiles of the grid where they would occupy no more than half of
 // the CUs, each as two workgroups, run on 128 x 256 (HALF): about half the
 // time.  kCus workgroups fill the GPU, one a CU.
-constexpr int kCus = 256;
 
 template <int DT, int CT, class S, class HALF>
 __global__ void __launch_bounds__(64 * S::NW) matmul_pipe(MatmulArgs p, int tiles_n, int vec) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(1024))) uint8_t a0[S::A_STAGE], b0[S::B_STAGE], a1[S::A_STAGE], b1[S::B_STAGE];
-  const Stages lds{a0, b0, a1, b1};
+  LDS_STAGES(S, lds);
   constexpr bool HALVES = S::BM == 256;
   // The grid holds the most tiles that offsets can give; those that there are
   // are dealt to the XCDs in equal runs.
@@ -356,7 +383,7 @@ __global__ void __launch_bounds__(64 * S::NW) matmul_pipe(MatmulArgs p, int tile
 template <int DT, int CT, class S, bool EPI>
 __global__ void __launch_bounds__(64 * S::NW) wgrad_pipe(WgradArgs p, int tiles_k, int tiles_n, int vec) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(1024))) uint8_t a0[S::A_STAGE], b0[S::B_STAGE], a1[S::A_STAGE], b1[S::B_STAGE];
+  LDS_STAGES(S, lds);
   // One group after another, each dealt to all XCDs: groups differ in rows.
   const int each = tiles_k * tiles_n;
   const int g = __builtin_amdgcn_readfirstlane((int)blockIdx.x / each);
@@ -370,7 +397,7 @@ __global__ void __launch_bounds__(64 * S::NW) wgrad_pipe(WgradArgs p, int tiles_
   const uint16_t* X = static_cast<const uint16_t*>(p.X) + first * p.ldx + m0;
   const uint16_t* dY = static_cast<const uint16_t*>(p.dY) + first * p.ldy + n0;
   f32x4 acc[S::NB][S::MB];
-  tile_sums<DT == GEMM_DTYPE_BF16, S>(Stages{a0, b0, a1, b1}, X, (int)p.ldx, p.K - m0, dY, (int)p.ldy, p.N - n0, end - first, acc);
+  tile_sums<DT == GEMM_DTYPE_BF16, S>(lds, X, (int)p.ldx, p.K - m0, dY, (int)p.ldy, p.N - n0, end - first, acc);
   finish<CT, S, EPI>(static_cast<typename mx::TypeOf<CT>::type*>(p.dW) + g * p.stride_w + m0 * p.ldw + n0, p.ldw, p.K - m0,
                      p.N - n0, acc, vec, p.alpha, p.beta);
 #endif
@@ -382,13 +409,13 @@ bool rows_whole(const void* C, int64_t ld, int64_t stride, int64_t cols, int64_t
 
 }  // namespace
 
-template <bool A, bool B, int SIDE>
-using TileOf = Tile<A, B, SIDE, SIDE, SIDE / 2, SIDE / 2>;
+template <bool A, bool B, int SIDE, int NS = 2>
+using TileOf = Tile<A, B, SIDE, SIDE, SIDE / 2, SIDE / 2, NS>;
 
-template <int DT, int CT, int SIDE>
-hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s) {
-  typedef TileOf<false, true, SIDE> S;
-  typedef TileOf<false, false, SIDE> St;
+template <int DT, int CT, int SIDE, int NS>
+hipError_t on_stages(const MatmulArgs& a, hipStream_t s) {
+  typedef TileOf<false, true, SIDE, NS> S;
+  typedef TileOf<false, false, SIDE, NS> St;
   typedef Tile<false, true, 128, 256, 64, 128> H;
   typedef Tile<false, false, 128, 256, 64, 128> Ht;
   const int vec = rows_whole(a.Y, a.ldy, 0, a.N, CT == GEMM_DTYPE_F32 ? 4 : 2);
@@ -401,11 +428,10 @@ hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((matmul_pipe<DT, CT, S, H>), grid, block, 0, s, a, (int)tiles_n, vec);
   return hipGetLastError();
 }
-template hipError_t launch_pipe<GROUPED_TYPE, GROUPED_OUT, GROUPED_TILE>(const MatmulArgs&, hipStream_t);
 
-template <int DT, int CT, int SIDE>
-hipError_t launch_pipe(const WgradArgs& a, hipStream_t s) {
-  typedef TileOf<true, true, SIDE> S;
+template <int DT, int CT, int SIDE, int NS>
+hipError_t on_stages(const WgradArgs& a, hipStream_t s) {
+  typedef TileOf<true, true, SIDE, NS> S;
   const int vec = rows_whole(a.dW, a.ldw, a.G > 1 ? a.stride_w : 0, a.N, CT == GEMM_DTYPE_F32 ? 4 : 2);
   const int64_t tiles_k = ((int64_t)a.K + S::BM - 1) / S::BM, tiles_n = ((int64_t)a.N + S::BN - 1) / S::BN;
   const dim3 grid((unsigned)(a.G * tiles_k * tiles_n)), block(64 * S::NW);
@@ -415,6 +441,23 @@ hipError_t launch_pipe(const WgradArgs& a, hipStream_t s) {
   else
     hipLaunchKernelGGL((wgrad_pipe<DT, CT, S, false>), grid, block, 0, s, a, (int)tiles_k, (int)tiles_n, vec);
   return hipGetLastError();
+}
+
+template <int DT, int CT, int SIDE>
+hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s) {
+  if constexpr (SIDE == 128) {
+    if (alone(a)) return on_stages<DT, CT, SIDE, 4>(a, s);
+  }
+  return on_stages<DT, CT, SIDE, 2>(a, s);
+}
+template hipError_t launch_pipe<GROUPED_TYPE, GROUPED_OUT, GROUPED_TILE>(const MatmulArgs&, hipStream_t);
+
+template <int DT, int CT, int SIDE>
+hipError_t launch_pipe(const WgradArgs& a, hipStream_t s) {
+  if constexpr (SIDE == 128) {
+    if (alone(a)) return on_stages<DT, CT, SIDE, 4>(a, s);
+  }
+  return on_stages<DT, CT, SIDE, 2>(a, s);
 }
 template hipError_t launch_pipe<GROUPED_TYPE, GROUPED_OUT, GROUPED_TILE>(const WgradArgs&, hipStream_t);
 

@@ -28,9 +28,9 @@ def kernel(launch):
     return next(k for k in KERNELS if k in launch.name.decode())
 
 
-def side(launch):
-    """The side of a pipelined kernel's tile."""
-    return int(re.search(r"4TileILb\dELb\dELi(\d+)", launch.name.decode()).group(1))
+def tile(launch):
+    """The side of a pipelined kernel's tile and its LDS stages."""
+    return tuple(map(int, re.search(r"4TileILb\dELb\dELi(\d+)ELi\d+ELi\d+ELi\d+ELi(\d)", launch.name.decode()).groups()))
 
 
 def compile_dry(folder: str) -> DryRun:

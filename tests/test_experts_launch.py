@@ -6,7 +6,7 @@ import shutil
 import pytest
 
 from dense_gemm_row_amd import gemm, w4
-from tests.experts_dry_run import compile_dry, kernel, side
+from tests.experts_dry_run import compile_dry, kernel, tile
 from tests.experts_sizes import GRADIENTS, PRODUCTS
 
 TOP = 2 ** 31 - 1
@@ -47,25 +47,25 @@ def gradient(dry, T, k, N, G, dtype=BF16, c=F32, x=X, ldx=None, ldw=None):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("tile", PRODUCTS)
-def test_tiles_of_products(dry, tile, dtype):
-    for T, k, N, offsets in PRODUCTS[tile]:
+@pytest.mark.parametrize("shape", PRODUCTS, ids=str)
+def test_tiles_of_products(dry, shape, dtype):
+    for T, k, N, offsets in PRODUCTS[shape]:
         for trans in (0, 1):
             for c in (dtype, F32):
                 one, = product(dry, T, k, N, len(offsets) - 1, trans, dtype, c)
-                if tile == 16:
+                if shape == 16:
                     assert kernel(one) == "matmul_few", (T, k, N, one.name)
                 else:
-                    assert kernel(one) == "matmul_pipe" and side(one) == tile, (T, k, N, one.name)
+                    assert kernel(one) == "matmul_pipe" and tile(one) == shape, (T, k, N, one.name)
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("tile", GRADIENTS)
-def test_tiles_of_gradients(dry, tile, dtype):
-    for T, k, N, offsets in GRADIENTS[tile]:
+@pytest.mark.parametrize("shape", GRADIENTS, ids=str)
+def test_tiles_of_gradients(dry, shape, dtype):
+    for T, k, N, offsets in GRADIENTS[shape]:
         for c in (dtype, F32):
             one, = gradient(dry, T, k, N, len(offsets) - 1, dtype, c)
-            assert kernel(one) == "wgrad_pipe" and side(one) == tile, (T, k, N, one.name)
+            assert kernel(one) == "wgrad_pipe" and tile(one) == shape, (T, k, N, one.name)
 
 
 def test_what_the_general_kernels_take(dry):

@@ -76,6 +76,7 @@ def test_pipelined_kernels_keep_hazard_distances(tmp_path):
             assert any(MNEMONIC.match(op) for op, _ in ins), m.group(1)
             assert not findings(ins), (m.group(1), findings(ins)[:3])
             checked += 1
-    # Two types with two results each, two tiles: products in two layouts,
-    # gradients with and without the old values.
-    assert checked == 4 * 2 * (2 + 2), checked
+    # Two types with two results each; tiles of 256, and of 128 with two and with
+    # four stages: products in two layouts, gradients with and without the old
+    # values.
+    assert checked == 4 * 3 * (2 + 2), checked
