@@ -171,7 +171,12 @@ def linear(x, w, offsets, transposed: bool = False):
     """`matmul` for training: x is T x K, w groups x K x N (``transposed``:
     groups x N x K), of one type.  Gradients have that type too: dx = dy @
     w[g].T (zero for rows of no group) and dw[g] = x_g.T @ dy_g, summed in 32
-    bits and rounded once.  There is no second derivative."""
+    bits and rounded once.  There is no second derivative.
+
+    A step captured into a graph: warm it up on the capturing stream, and let go
+    of every result of an earlier step over the same tensors before the capture
+    (torch ends a capture, and with it the process, whose backward pass meets
+    the accumulation of a graph on another stream)."""
     global _Linear
     if _Linear is None:
         _Linear = _make_linear()

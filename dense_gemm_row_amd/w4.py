@@ -204,7 +204,8 @@ def quantize(w, group: int = 128, zeros: bool = True, transposed: bool = False, 
     x N as the other products take weights; a leading dimension more is a
     stack of experts.  Scales are of ``scale_dtype`` (default: w's type,
     bfloat16 for float32): the type of the activations to come.  zeros False:
-    no zero points."""
+    no zero points.  An ``out`` is written in its own group, scale type and
+    zero points."""
     stack = w.dim() == 3
     first = w[0] if stack and w.shape[0] > 0 else w
     if stack and w.shape[0] == 0:
@@ -284,7 +285,7 @@ def matmul(x, q: W4Tensor, out=None, stream=None):
     """x @ w.T for 4-bit weights q (N x K) and x (M x K) of the scales' type,
     which is the result's.  Up to 128 rows the codes are multiplied as they
     are; more rows multiply dequantised weights, rounded to that type, through
-    a workspace of 2 N K bytes."""
+    a workspace of 2 N K bytes.  (For serving: no gradients.)"""
     dtype, M, K, ldx, N, on, out, ldy = _operands(x, q, 2, out, stream)
     need = 0 if M <= ROWS else lib().gemm_w4_matmul_workspace_bytes(M, N, K)
     ws = on.empty(need, mx._torch.uint8) if need > 0 else None
@@ -298,7 +299,7 @@ def grouped_matmul(x, q: W4Tensor, offsets, out=None, stream=None):
     offsets[g + 1] - 1 of x (T x K), and a stack q of 4-bit weights (experts x
     N x K).  Rows of no group are zero in a new result; in ``out`` they stay as
     they are.  (Above 128 rows an expert on average all experts' weights are
-    dequantised first.)"""
+    dequantised first.  For serving: no gradients.)"""
     fill = out is None
     dtype, T, K, ldx, N, on, out, ldy = _operands(x, q, 3, out, stream)
     G = q.codes.shape[0]

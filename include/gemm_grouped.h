@@ -31,9 +31,12 @@
  *   an output overlapping an input                        -> ALIAS
  *   launch failure                                        -> HIP
  *
- * Speed: 16-bit operands that are 16-byte aligned, with leading dimensions,
- * strides, N and K that are multiples of 8 and leading dimensions below 2^20,
- * run on pipelined matrix-core kernels; everything else on a general one.
+ * Speed: 16-bit operands run on pipelined matrix-core kernels where X's and
+ * W's (the gradient's X's and dY's) rows begin on 16 bytes (pointers, leading
+ * dimensions and strides) and are whole 16-byte pieces long (K % 8 == 0, and
+ * N % 8 == 0 but for trans_w = 1), with leading dimensions below 2^20; the
+ * result may lie anywhere.  Everything else runs on a general kernel, at a
+ * half to two thirds of their rate for large products.
  */
 #ifndef DENSE_GEMM_ROW_AMD_GEMM_GROUPED_H
 #define DENSE_GEMM_ROW_AMD_GEMM_GROUPED_H

@@ -26,6 +26,12 @@
  * ldq and stride_q multiples of 16 (else UNSUPPORTED).  Types of activations
  * and scales are GEMM_DTYPE_F16 or _BF16.  Errors besides: a group size that
  * is not 32, 64 or 128, or K above 2^30 -> INVALID_ARG.
+ *
+ * Speed: products of few rows (see GEMM_W4_ROWS) read codes, activations,
+ * scales and zero points in whole pieces wherever their rows begin; some 10 %
+ * faster where X's rows begin on 16 bytes and K % 8 == 0, and a row's scales
+ * (and zero points) are whole runs of 256 k, aligned to such a run.  Rows of
+ * fewer than 256 k, and leading dimensions from 2^22 on, are read by element.
  */
 #ifndef DENSE_GEMM_ROW_AMD_GEMM_W4_H
 #define DENSE_GEMM_ROW_AMD_GEMM_W4_H
@@ -74,10 +80,11 @@ gemm_status_t gemm_w4_dequantize(int32_t dtype, int32_t s_dtype, int64_t N, int6
 /*
  * Y = X x W^T: X is M x K and Y M x N of type dtype, W the coded N x K matrix
  * with scales of that type.  Up to GEMM_W4_ROWS rows, the codes enter the matrix
- * core as whole numbers (exact in both types), each group's sum is accumulated
- * in FP32, its zero point times the sum of its activations is taken off and
- * the scale applied in FP32; the result is rounded once.  (So an activation
- * that is infinite gives NaN, not an infinity.)  With more rows the weights are
+ * core as the whole numbers 16 + q (exact in both types), each group's sum is
+ * accumulated in FP32, 16 + zero point times the sum of its activations is
+ * taken off and the scale applied in FP32; the result is rounded once.  (So an
+ * activation that is infinite gives NaN, not an infinity, and sums of a group's
+ * activations have to stay below 2^123.)  With more rows the weights are
  * dequantised first, rounded to dtype, into `workspace`
  * (gemm_w4_matmul_workspace_bytes bytes, 16-byte aligned, not overlapping the
  * operands; too small a one -> INVALID_ARG) and multiplied as gemm_*_bt does;
@@ -96,8 +103,8 @@ int64_t gemm_w4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * The same by groups: Y[t] = X[t] x W_g^T for every row t of every group g
  * (X T x K, Y T x N; `offsets` and `fill` as in gemm_grouped_matmul).  Up to
  * GEMM_W4_ROWS rows a group on average (T <= GEMM_W4_ROWS * G) the codes are
- * read by the product itself, each group's codes once for every
- * 64 of its rows; beyond, all G matrices are dequantised into
+ * read by the product itself, each group's codes once for every 16, 32 or 64 of
+ * its rows; beyond, all G matrices are dequantised into
  * `workspace` and multiplied as gemm_grouped_matmul does.
  */
 gemm_status_t gemm_w4_grouped(int32_t dtype, int64_t G, int64_t T, int64_t N, int64_t K, const int32_t *offsets,
