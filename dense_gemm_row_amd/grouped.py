@@ -174,16 +174,37 @@ def linear(x, w, offsets, transposed: bool = False):
     bits and rounded once.  There is no second derivative.
 
     A step captured into a graph: warm it up on the capturing stream, and let go
-    of every result of an earlier step over the same tensors before the capture
-    (torch ends a capture, and with it the process, whose backward pass meets
-    the accumulation of a graph on another stream)."""
+    of every result of an earlier step over the same leaves before the capture
+    (torch's backward pass would end the process where a leaf's gradient
+    belongs to another stream; `linear` refuses leaves of its own steps, it
+    cannot see those of other operators)."""
     global _Linear
     if _Linear is None:
         _Linear = _make_linear()
-    return _Linear.apply(x, w, offsets, transposed)
+    held = None  # (until the new graph holds it)
+    if mx._torch.is_grad_enabled():
+        held = [_accumulation(t) for t in (x, w)
+                if isinstance(t, mx._torch.Tensor) and t.requires_grad and t.is_leaf and t.is_cuda]
+    y = _Linear.apply(x, w, offsets, transposed)
+    del held
+    return y
+
+
+def _accumulation(leaf):
+    """The node that accumulates a leaf's gradient.  It lives as long as any
+    graph with the leaf and belongs to the stream of the first of them: in a
+    capture on another stream the leaf is refused."""
+    node = leaf.view_as(leaf).grad_fn.next_functions[0][0]
+    here = mx._raw_stream(leaf.get_device())
+    first = node.metadata.setdefault("grouped.linear", here)
+    if first != here and mx._torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("capture: results of an earlier step on another stream over the same leaf are alive")
+    return node
 
 
 def _make_linear():
+    if mx._torch is None:
+        mx._load()
     import torch
 
     class Linear(torch.autograd.Function):

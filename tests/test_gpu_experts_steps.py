@@ -54,6 +54,30 @@ def test_captured_training_step(dtype):
             assert torch.equal(got, exact.to(dtype)), k
 
 
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
+def test_a_capture_refuses_leaves_of_a_living_step_on_another_stream():
+    """(Refused at the forward pass: nothing of the backward pass is captured.)"""
+    x, w = whole(8, (40, 64), torch.float32), whole(9, (2, 64, 32), torch.float32).requires_grad_(True)
+    at = offsets_of(0, 20, 40)
+    alive = grouped.linear(x, w, at)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with pytest.raises(RuntimeError, match="earlier step on another stream"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            grouped.linear(x, w, at)
+    with torch.cuda.stream(side):  # outside a capture streams may differ
+        again = grouped.linear(x, w, at)
+    torch.cuda.synchronize()
+    assert torch.equal(alive, again)
+    del alive, again
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y = grouped.linear(x, w, at)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y[:20], x[:20] @ w[0])
+
+
 @pytest.mark.parametrize("transposed", [False, True])
 def test_gradient_of_weights_that_all_groups_share(transposed):
     x, dy = whole(4, (90, 64), torch.float32), whole(5, (90, 48), torch.float32)
