@@ -2,7 +2,7 @@
 // grouped: Y[t] = X[t] x W^T with
 //   W[n][k] = s[n][j] (q[n][k] - z[n][j]),  j = k / group, so that
 //   Y[t][n] = sum_j s[n][j] (sum_{k in j} q X[t][k] - z[n][j] sum_{k in j} X[t][k]).
-//  * A workgroup of eight waves computes 16 MB rows x 16 NB NW columns: KW waves
+//  * A workgroup of 8 or 16 waves computes 16 MB rows x 16 NB NW columns: KW waves
 //    along k, whose sums are added in order through LDS at the end, times NW
 //    along the columns.  A wave's codes are read straight into registers, 16
 //    rows of SPAN / 2 bytes; the waves of one part of k share X through LDS.
@@ -39,7 +39,6 @@ namespace gemm {
 namespace w4 {
 namespace {
 
-constexpr int WAVES = 8;
 constexpr unsigned OOB = 0x80000000u;  // offset past every descriptor's range
 constexpr int64_t kMostBlocks = 1 << 22;
 
@@ -99,9 +98,9 @@ __device__ __forceinline__ u32x4 reorder(u32x4 x) {
 
 // WAVES waves are KW along k times NW along the columns, each with NB blocks of
 // 16 columns; SPAN k at a time.
-template <int GB_, int MB_, int NB_, int KW_>
+template <int GB_, int MB_, int NB_, int KW_, int WAVES_ = 8>
 struct Shape {
-  static constexpr int GB = GB_, MB = MB_, NB = NB_, KW = KW_, NW = WAVES / KW_;
+  static constexpr int GB = GB_, MB = MB_, NB = NB_, KW = KW_, WAVES = WAVES_, NW = WAVES / KW_;
   static constexpr int SPAN = MB == 1 ? 256 : 128;
   static constexpr int V = GB / 32;         // matrix instructions of a group
   static constexpr int GROUPS = SPAN / GB;  // groups of a span
@@ -167,7 +166,7 @@ __device__ __forceinline__ void without(unsigned (&w)[N], int n) {
 }
 
 template <bool BF, class S, Reads HOW>
-__global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned tiles, unsigned tiles_n) {
+__global__ void __launch_bounds__(64 * S::WAVES) matmul_few(MatmulArgs p, unsigned tiles, unsigned tiles_n) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef half_t<BF> T;
   constexpr int GB = S::GB, MB = S::MB, NB = S::NB, KW = S::KW, NW = S::NW, SPAN = S::SPAN, V = S::V, GROUPS = S::GROUPS;
@@ -385,7 +384,7 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
     // registers (loads return in order, so what is asked for late would hold up
     // what was asked for early).  SHARED X goes on into one of two places in
     // LDS, a span ahead; then every wave takes part in every barrier.
-    constexpr int DEPTH = S::SHARED ? 4 : 2;
+    constexpr int DEPTH = S::SHARED && S::WAVES == 8 ? 4 : 2;  // (16 waves hide as much with half the registers)
     Codes<S> ring[DEPTH];
     const int spans = ((K + SPAN - 1) / SPAN + KW - 1) / KW;
     const int none = (K + SPAN - 1) / SPAN * SPAN;  // (a whole span past the end, so that a lane's 32 k are there or not)
@@ -440,7 +439,7 @@ __global__ void __launch_bounds__(64 * WAVES) matmul_few(MatmulArgs p, unsigned 
         for (int e = 0; e < 4; ++e)
           sums[(kw * S::ROWS + 16 * i + 4 * q + e) * S::COLS + 16 * (NB * nw + j) + r] = acc[j][i][e];
     barrier();
-    for (int i = tid; i < S::ROWS * S::COLS; i += 64 * WAVES) {
+    for (int i = tid; i < S::ROWS * S::COLS; i += 64 * S::WAVES) {
       const int m = i / S::COLS, col = i % S::COLS;
       if (m >= t.rows || n0 + col >= p.N) continue;
       float v = 0.f;
@@ -480,7 +479,7 @@ hipError_t start(const MatmulArgs& a, hipStream_t s) {
   const int64_t tiles = tiles_of(a, S::ROWS, S::COLS);
   if (tiles <= 0) return hipSuccess;
   if (tiles >= 1ll << 31) return hipErrorInvalidConfiguration;  // (of a result that no memory holds)
-  hipLaunchKernelGGL((matmul_few<BF, S, HOW>), dim3((unsigned)(tiles < kMostBlocks ? tiles : kMostBlocks)), dim3(64 * WAVES), 0,
+  hipLaunchKernelGGL((matmul_few<BF, S, HOW>), dim3((unsigned)(tiles < kMostBlocks ? tiles : kMostBlocks)), dim3(64 * S::WAVES), 0,
                      s, a, (unsigned)tiles, (unsigned)((a.N + S::COLS - 1) / S::COLS));
   return hipGetLastError();
 }
@@ -491,10 +490,11 @@ hipError_t along(const MatmulArgs& a, int kw, hipStream_t s) {
     if (kw == 8) return start<BF, Shape<GB, MB, 1, 8>, HOW>(a, s);
   }
   if (kw >= 4) return start<BF, Shape<GB, MB, 1, 4>, HOW>(a, s);
-  if constexpr (MB != 3) {  // (12 KB of X do not split over eight waves)
-    if (kw == 1) return start<BF, Shape<GB, MB, 1, 1>, HOW>(a, s);
-  }
-  return start<BF, Shape<GB, MB, 1, 2>, HOW>(a, s);
+  // (12 KB of X do not split over eight waves along the columns: four, and four
+  // along k.  M 33, 4096 x 11008: 20.6 us, 23.3 with two along k; with one or two
+  // blocks of rows 16 waves gain nothing: M 1, 4096 x 4096, 9.0 us and 6.8 with 8.)
+  if constexpr (MB == 3) return start<BF, Shape<GB, MB, 1, 4, 16>, HOW>(a, s);
+  else return kw == 1 ? start<BF, Shape<GB, MB, 1, 1>, HOW>(a, s) : start<BF, Shape<GB, MB, 1, 2>, HOW>(a, s);
 }
 
 template <bool BF, int GB, int MB>
@@ -518,7 +518,7 @@ hipError_t launch_few(const MatmulArgs& a, hipStream_t s) {
   const int64_t rows = a.offsets && a.G > 0 ? ((int64_t)a.T + a.G - 1) / a.G : a.T;
   auto likely = [&](int64_t tile_rows, int64_t kw) {
     const int64_t m = a.offsets ? (a.T < a.G ? (int64_t)a.T : a.T / tile_rows + a.G / 2) : (a.T + tile_rows - 1) / tile_rows;
-    return m * ((a.N + 16 * (WAVES / kw) - 1) / (16 * (WAVES / kw)));
+    return m * ((a.N + 16 * (8 / kw) - 1) / (16 * (8 / kw)));
   };
   auto along_k = [&](int64_t tile_rows) {
     int kw = 1;
@@ -527,7 +527,7 @@ hipError_t launch_few(const MatmulArgs& a, hipStream_t s) {
   };
   // More rows a tile read fewer codes and more of X at once (M 64: 4096 x 4096
   // 14.1 us on 32 rows, 18.9 on 64; 4096 x 11008 30.2 and 24.7.  M 33, 4096 x
-  // 11008: 21.8 us on 48 rows, 24.5 on 64).
+  // 11008: 20.6 us on 48 rows, 24.5 on 64).
   if (rows <= (a.offsets ? 16 : 32)) return on_rows<BF, GB, 1>(a, along_k(16), s);
   if (rows <= 32 || likely(64, 4) < 160) return on_rows<BF, GB, 2>(a, along_k(32), s);
   if (rows <= 48 && !a.offsets) return on_rows<BF, GB, 3>(a, along_k(48), s);
