@@ -78,8 +78,8 @@ hipError_t pipelined(int dtype, int c_dtype, int side, const Args& a, hipStream_
 
 // Time of `tiles` tiles, `at_once` of them at a time, half a round lost at the
 // end; `fixed` us a tile beside `per_slice` for each of its slices of 64 k.
-double tile_us(double tiles, int at_once, double tail, double fixed, double per_slice, double slices) {
-  const double rounds = tiles / at_once + tail;
+double tile_us(double tiles, int at_once, double fixed, double per_slice, double slices) {
+  const double rounds = tiles / at_once + 0.5;
   return (rounds < 1. ? 1. : rounds) * (fixed + per_slice * slices);
 }
 
@@ -96,25 +96,26 @@ int tile_for(const MatmulArgs& a) {
   const double slices = (a.K + 63) / 64, groups = a.T < a.G ? a.T : a.G, of_one = 2. * a.N * a.K / 5.2e6, read = groups * of_one;
   auto us = [&](int side, int at_once, double fixed, double per_slice, double lone) {
     const double tiles = likely_tiles(a, side);
-    return tile_us(tiles, at_once, 0.5, fixed, tiles <= kCus ? lone : per_slice, slices);
+    return tile_us(tiles, at_once, fixed, tiles <= kCus ? lone : per_slice, slices);
   };
   const double m = a.T / 16. + 0.5 * groups, read16 = (m < a.T ? m : a.T) * of_one;
-  const double us16 = tile_us(m * ((a.N + 63) / 64), 256, 0.5, 3., 0.2, slices);
+  const double us16 = tile_us(m * ((a.N + 63) / 64), 256, 3., 0.2, slices);
   const double us128 = alone(a) ? 4.8 + 0.34 * slices : us(128, 512, 5.5, 1.1, 0.66), us256 = us(256, 256, 13., 1.35, 1.35);
   if ((us16 > read16 ? us16 : read16) < (us128 > read ? us128 : read) && us16 < us256) return 16;
   return us256 < us128 ? 256 : 128;
 }
 // The gradient's likewise: a tile writes as many results however few rows its
-// group has, 20 us beside the slices on 256 x 256 and 8 on 128 x 128.  (8 groups
-// of 2048 rows, 4096 x 4096, FP32: 503 us and 574; 64 groups of 32 rows, 1024 x
-// 1024: 90 and 68; 8 of 512, 2048 x 2048: 73 and 65.)
+// group has, 14 us beside 1.35 a slice on 256 x 256, 6.4 beside 0.82 on 128 x 128;
+// groups that differ in rows lose three quarters of a round.  (8 groups of 2048
+// rows on average, 4096 x 4096, FP32: 460 us on 256 and 540 on 128; 2048 x 2048: 158
+// and 132; of 512, 2048 x 2048: 50 and 51; 64 of 256, 1024 x 1024: 88 and 80.)
 int tile_for(const WgradArgs& a) {
   const double slices = (double)a.T / (a.G > 0 ? a.G : 1) / 64;
   auto us = [&](int side, int at_once, double fixed, double per_slice) {
-    const double tiles = likely_tiles(a, side);
-    return tile_us(tiles, at_once, 0., fixed, per_slice, slices < 2 ? 2 : slices);
+    const double rounds = likely_tiles(a, side) / at_once;
+    return (a.G > 1 ? rounds + 0.75 : __builtin_ceil(rounds)) * (fixed + per_slice * (slices < 2 ? 2 : slices));
   };
-  return us(256, 256, 20., 1.35) < us(128, 512, 8., 1.1) ? 256 : 128;
+  return us(256, 256, 14., 1.35) < us(128, 512, 6.4, 0.82) ? 256 : 128;
 }
 
 hipError_t launch(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s) {

@@ -459,14 +459,16 @@ template <int DT, int CT, class S, bool EPI>
 __global__ void __launch_bounds__(64 * S::NW) wgrad_pipe(WgradArgs p, int tiles_k, int tiles_n, int vec) {
 #if defined(__HIP_DEVICE_COMPILE__)
   LDS_STAGES(S, lds);
-  // One group after another, each dealt to all XCDs: groups differ in rows.
+  // One group after another, the longest first (they differ in rows, so the last
+  // tiles should be the shortest), each dealt to all XCDs.
   const int each = tiles_k * tiles_n;
-  const int g = __builtin_amdgcn_readfirstlane((int)blockIdx.x / each);
+  const int rank = __builtin_amdgcn_readfirstlane((int)blockIdx.x / each);
   int tm, tn;
-  tile_of_block((int)blockIdx.x - g * each, TileMap{tiles_k, tiles_n, GEMM_ORDER_XCD, 4, kXcds}, tm, tn);
+  tile_of_block((int)blockIdx.x - rank * each, TileMap{tiles_k, tiles_n, GEMM_ORDER_XCD, 4, kXcds}, tm, tn);
   const int m0 = __builtin_amdgcn_readfirstlane(tm * S::BM), n0 = __builtin_amdgcn_readfirstlane(tn * S::BN);
-  int first, end;
-  group_rows(p.offsets, p.T, g, first, end);
+  int g, first, end;
+  ranked_group(p.offsets, p.T, p.G, rank, g, first, end);
+  g = __builtin_amdgcn_readfirstlane(g);
   first = __builtin_amdgcn_readfirstlane(first);
   end = __builtin_amdgcn_readfirstlane(end);
   const uint16_t* X = static_cast<const uint16_t*>(p.X) + first * p.ldx + m0;
