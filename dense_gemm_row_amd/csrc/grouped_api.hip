@@ -118,16 +118,18 @@ int tile_for(const WgradArgs& a) {
   return us(256, 256, 14., 1.35) < us(128, 512, 6.4, 0.82) ? 256 : 128;
 }
 
-hipError_t launch(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s) {
-  const int side = tile_for(a);
-  if (!pipe_fits(dtype, a, side)) return launch_general(dtype, c_dtype, a, s);
-  return side == 16 ? launch_few(dtype, c_dtype, a, s) : pipelined(dtype, c_dtype, side, a, s);
-}
 hipError_t launch(int dtype, int c_dtype, const WgradArgs& a, hipStream_t s) {
   return pipe_fits(dtype, a) ? pipelined(dtype, c_dtype, tile_for(a), a, s) : launch_general(dtype, c_dtype, a, s);
 }
 
 }  // namespace
+
+hipError_t launch_matmul(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s) {
+  const int side = tile_for(a);
+  if (!pipe_fits(dtype, a, side)) return launch_general(dtype, c_dtype, a, s);
+  return side == 16 ? launch_few(dtype, c_dtype, a, s) : pipelined(dtype, c_dtype, side, a, s);
+}
+
 }  // namespace grouped
 }  // namespace gemm
 
@@ -152,7 +154,7 @@ gemm_status_t gemm_grouped_matmul(int32_t dtype, int32_t c_dtype, int32_t trans_
   if ((st = check_dense("Y", Y, T, N, ldy, dtype_bytes(c_dtype), &y)) != GEMM_OK) return st;
   if (overlap(y, x) || overlap(y, w) || overlap(y, o)) return fail(GEMM_ERR_ALIAS, "Y overlaps an operand");
   const MatmulArgs a{offsets, X, W, Y, ldx, ldw, stride_w, ldy, (int)G, (int)T, (int)N, (int)K, fill, trans_w};
-  return launched(grouped::launch(dtype, c_dtype, a, static_cast<hipStream_t>(stream)));
+  return launched(grouped::launch_matmul(dtype, c_dtype, a, static_cast<hipStream_t>(stream)));
 }
 
 gemm_status_t gemm_grouped_wgrad(int32_t dtype, int32_t c_dtype, int64_t G, int64_t T, int64_t K, int64_t N,

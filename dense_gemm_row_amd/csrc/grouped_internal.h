@@ -34,6 +34,9 @@ struct WgradArgs {
 hipError_t launch_general(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s);
 hipError_t launch_general(int dtype, int c_dtype, const WgradArgs& a, hipStream_t s);
 
+// The product on whichever kernel and tile is best for it (grouped_api.hip).
+hipError_t launch_matmul(int dtype, int c_dtype, const MatmulArgs& a, hipStream_t s);
+
 // 16-bit operands (DT) of whole 16-byte pieces, result of type CT, on tiles of
 // SIDE x SIDE (256, 128): grouped_pipe.hip.
 template <int DT, int CT, int SIDE>

@@ -171,10 +171,11 @@ gemm_status_t gemm_w4_matmul(int32_t dtype, int64_t M, int64_t N, int64_t K, con
   if (!many_rows(M, 1, K))
     return launched(few_rows(dtype, q->group, args_of(q, X, ldx, Y, ldy, M, N, K, 1, nullptr, 0), s));
   if ((st = launched(dequantize_all(dtype, q, 1, N, K, workspace, s))) != GEMM_OK) return st;
-  // (Rows of X that do not begin on 16 bytes: 300 rows, 8192 x 4095, 704 us on the
-  // plain product, 81 on the grouped one's kernel for them.)
-  if ((uintptr_t)X % 16 != 0 || ldx % 8 != 0 || K % 8 != 0)
-    return launched(grouped::launch_general(
+  // (Rows of X or Y that do not begin on 16 bytes: 300 rows, 8192 x 4095, 704 us on
+  // the plain product, 81 on the grouped one of a single group; 320 rows, 149 x
+  // 1952, 171 and 18.)
+  if ((uintptr_t)X % 16 != 0 || ldx % 8 != 0 || K % 8 != 0 || (uintptr_t)Y % 16 != 0 || ldy % 8 != 0 || N % 8 != 0)
+    return launched(grouped::launch_matmul(
         dtype, dtype, grouped::MatmulArgs{nullptr, X, workspace, Y, ldx, row_values(K), 0, ldy, 1,
                                           (int)M, (int)N, (int)K, 0, 1}, s));
   return (dtype == GEMM_DTYPE_BF16 ? gemm_bf16_bt : gemm_f16_bt)(M, N, K, static_cast<const uint16_t*>(X), ldx,

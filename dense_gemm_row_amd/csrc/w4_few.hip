@@ -41,6 +41,7 @@ namespace {
 
 constexpr unsigned OOB = 0x80000000u;  // offset past every descriptor's range
 constexpr int64_t kMostBlocks = 1 << 22;
+constexpr int64_t kFar = 1 << 22;  // leading dimensions below it: a tile's rows and columns are within 31 bits of bytes
 
 template <class F, int... I>
 __device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
@@ -131,8 +132,8 @@ struct Codes {
   u32x4 x[S::XL];
 };
 
-// How a lane reads: ANY by element; SPANS, in 16-byte pieces wherever they
-// begin; WHOLE, aligned pieces through descriptors whose range ends them.
+// How a lane reads: ANY by element (X in pieces where it can); SPANS, in 16-byte
+// pieces wherever they begin; WHOLE, aligned pieces through descriptors whose range ends them.
 enum Reads { ANY, SPANS, WHOLE };
 
 // N words (of BYTES bytes, 1 to 4 N) at an offset of a buffer.
@@ -274,13 +275,14 @@ __global__ void __launch_bounds__(64 * S::WAVES) matmul_few(MatmulArgs p, unsign
         }
       }
     };
+    const bool pieces = HOW == SPANS || (HOW == ANY && p.K >= 8 && p.ldx < kFar);
     auto load_x = [&](int k0, u32x4 (&xv)[S::XL]) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < S::XL; ++i) {
         if constexpr (HOW == WHOLE) {
           const unsigned off = k0 + xk[i] < K ? x_at[i] + 2 * k0 : OOB;
           buffer_words<4>(from_x, off, reinterpret_cast<unsigned(&)[4]>(xv[i]));
-        } else if constexpr (HOW == SPANS) {
+        } else if (pieces) {
           const int k = k0 + xk[i] < p.K - 8 ? k0 + xk[i] : p.K - 8;  // (K may be 0)
           __builtin_memcpy(&xv[i], (const uint8_t*)x0 + (x_at[i] + (unsigned)(2 * k)), 16);
         } else {
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(64 * S::WAVES) matmul_few(MatmulArgs p, unsign
       }
     };
     auto trim_x = [&](int k0, u32x4 (&xv)[S::XL]) __attribute__((always_inline)) {
-      if (HOW != SPANS || k0 + SPAN <= K) return;
+      if (!pieces || k0 + SPAN <= K) return;
 #pragma unroll
       for (int i = 0; i < S::XL; ++i) {
         const int past = k0 + xk[i] - (K - 8);
@@ -460,9 +462,9 @@ __global__ void __launch_bounds__(64 * S::WAVES) matmul_few(MatmulArgs p, unsign
 // and 69.4.  K 4095, one row of 4096 columns: 13.6 us SPANS, 29.3 by element.)
 template <class S>
 Reads reads_of(const MatmulArgs& a) {
-  constexpr int64_t g = S::GROUPS, far = 1 << 22;
+  constexpr int64_t g = S::GROUPS;
   const int64_t ng = groups_of(a.K, S::GB);
-  if (a.G == 0 || a.K < 8 || ng < g || a.ldx >= far || a.ldq >= far || a.lds >= far || a.ldz >= far) return ANY;
+  if (a.G == 0 || a.K < 8 || ng < g || a.ldx >= kFar || a.ldq >= kFar || a.lds >= kFar || a.ldz >= kFar) return ANY;
   const bool x = (uintptr_t)a.X % 16 == 0 && a.ldx % 8 == 0 && a.K % 8 == 0;
   const bool s = (uintptr_t)a.scales % (2 * g) == 0 && a.lds % g == 0 && (a.G <= 1 || a.stride_s % g == 0);
   const bool z = !a.zeros || ((uintptr_t)a.zeros % g == 0 && a.ldz % g == 0 && (a.G <= 1 || a.stride_z % g == 0));
@@ -502,7 +504,7 @@ hipError_t on_rows(const MatmulArgs& a, int kw, hipStream_t s) {
   switch (reads_of<Shape<GB, MB, 1, 4>>(a)) {
     case WHOLE: return along<BF, GB, MB, WHOLE>(a, kw, s);
     case SPANS: return along<BF, GB, MB, SPANS>(a, kw, s);
-    default: return start<BF, Shape<GB, 1, 1, 4>, ANY>(a, s);
+    default: return start<BF, Shape<GB, 1, 1, 1>, ANY>(a, s);  // (a row is a span at most, but for far strides)
   }
 }
 

@@ -112,6 +112,8 @@ def test_4_bit_products(dry, group, dtype):
         assert kernel(one) == "dequantize_rows" and kernel(two) == "matmul_general"
         one, = launched(dry, "gemm_w4_matmul", dtype, 16, 136, k, x, ldx, coded(group, k, 136), Y, 136, None, 0, None)
         assert kernel(one) == "matmul_few"
+    one, two = launched(dry, "gemm_w4_matmul", dtype, 300, 149, 512, X, 512, coded(group, 512, 149), Y, 149, K, 1 << 20, None)
+    assert kernel(one) == "dequantize_rows" and kernel(two) in ("matmul_pipe", "matmul_few")
     one, two = launched(dry, "gemm_w4_grouped", dtype, 2, 257, 136, 512, O, X, 512, coded(group, 512, 136), Y, 136, 1, K, 1 << 20,
                         None)
     assert kernel(one) == "dequantize_rows" and one.grid[1] == 2 and kernel(two) in ("matmul_pipe", "matmul_few")
