@@ -513,10 +513,11 @@ hipError_t on_rows(const MatmulArgs& a, int kw, hipStream_t s) {
 template <int DT, int GB>
 hipError_t launch_few(const MatmulArgs& a, hipStream_t s) {
   constexpr bool BF = DT == GEMM_DTYPE_BF16;
-  // The fewest waves along k whose tiles still occupy most of the CUs (4096 x
-  // 4096, one row: 8 waves along k, 256 tiles, 7.4 us; 4, 128 tiles, 10.9; 2,
-  // 64 tiles, 13.8.  4096 x 11008: 2, 172 tiles, 14.4 us; 4, 344 tiles, 19.9).
-  // Experts: tiles that are likely, not those of the worst offsets.
+  // The most waves along k whose tiles are no more than the CUs, one round of
+  // them (4096 x 4096, one row: 8 waves along k, 256 tiles, 6.7 us; 4, 128 tiles,
+  // 10.9.  4096 x 11008: 2, 172 tiles, 14.7 us; 4, 344 tiles, 19.9.  7105 x 8448, five
+  // rows: 2, 132 tiles, 32 us; 4, 264 tiles, 47.)  Experts: tiles that are likely,
+  // not those of the worst offsets.
   const int64_t rows = a.offsets && a.G > 0 ? ((int64_t)a.T + a.G - 1) / a.G : a.T;
   auto likely = [&](int64_t tile_rows, int64_t kw) {
     const int64_t m = a.offsets ? (a.T < a.G ? (int64_t)a.T : a.T / tile_rows + a.G / 2) : (a.T + tile_rows - 1) / tile_rows;
@@ -524,7 +525,7 @@ hipError_t launch_few(const MatmulArgs& a, hipStream_t s) {
   };
   auto along_k = [&](int64_t tile_rows) {
     int kw = 1;
-    while (kw < 8 && likely(tile_rows, kw) < 160) kw *= 2;
+    while (kw < 8 && likely(tile_rows, 2 * kw) <= 256) kw *= 2;
     return kw;
   };
   // More rows a tile read fewer codes and more of X at once (M 64: 4096 x 4096

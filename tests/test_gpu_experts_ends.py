@@ -63,7 +63,11 @@ def test_4_bit_experts(T, N, K, bounds, group):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16], ids=str)
 @pytest.mark.parametrize("T, K, N, bounds", [(1, 1, 1, [0, 1]), (9, 301, 77, [0, 1, 9]), (40, 1001, 515, [3, 20, 20, 39]),
                                              (700, 1001, 1203, [0, 350, 700]), (1500, 257, 2049, [0, 1500]), (33, 7, 9, [0, 33]),
-                                             (33, 9, 7, [1, 33]), (200, 1000, 1001, [0, 90, 200]), (200, 1001, 1000, [0, 90, 200])])
+                                             (33, 9, 7, [1, 33]), (200, 1000, 1001, [0, 90, 200]), (200, 1001, 1000, [0, 90, 200]),
+                                             # few tiles, long sums
+                                             (9, 2049, 77, [0, 1, 9]), (70, 1601, 130, [0, 33, 70]), (1, 4097, 5, [0, 1]),
+                                             (300, 1025, 65, [2, 2, 290]), (5000, 65, 131, [3, 2500, 4990]),
+                                             (2100, 7, 9, [0, 2100]), (4100, 63, 5, [1, 1, 4100])])
 def test_products_and_gradients(T, K, N, bounds, dtype):
     G = len(bounds) - 1
     x, dy = at_end(whole(6, -4, 5, (T, K), dtype)), at_end(whole(7, -4, 5, (T, N), dtype))
