@@ -416,7 +416,6 @@ __device__ __forceinline__ void product_tile(const MatmulArgs& p, const Stages<S
 // and the last tiles of the grid where they would occupy no more than half of
 // the CUs, each as two workgroups, run on 128 x 256 (HALF): about half the
 // time.  kCus workgroups fill the GPU, one a CU.
-
 template <int DT, int CT, class S, class HALF>
 __global__ void __launch_bounds__(64 * S::NW) matmul_pipe(MatmulArgs p, int tiles_n, int vec) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -30,8 +30,9 @@
  * Speed: products of few rows (see GEMM_W4_ROWS) read codes, activations,
  * scales and zero points in whole pieces wherever their rows begin; some 10 %
  * faster where X's rows begin on 16 bytes and K % 8 == 0, and a row's scales
- * (and zero points) are whole runs of 256 k, aligned to such a run.  Rows of
- * fewer than 256 k, and leading dimensions from 2^22 on, are read by element.
+ * (and zero points) are whole runs of 256 k, aligned to such a run.  Scales
+ * of rows of fewer than 256 k, and leading dimensions from 2^22 on, are read by
+ * element.
  */
 #ifndef DENSE_GEMM_ROW_AMD_GEMM_W4_H
 #define DENSE_GEMM_ROW_AMD_GEMM_W4_H
