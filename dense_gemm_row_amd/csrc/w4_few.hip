@@ -478,11 +478,11 @@ int64_t tiles_of(const MatmulArgs& a, int64_t rows, int64_t cols) {
 
 template <bool BF, class S, Reads HOW>
 hipError_t start(const MatmulArgs& a, hipStream_t s) {
-  const int64_t tiles = tiles_of(a, S::ROWS, S::COLS);
+  const int64_t tiles = tiles_of(a, S::ROWS, S::COLS), tiles_n = ((int64_t)a.N + S::COLS - 1) / S::COLS;
   if (tiles <= 0) return hipSuccess;
   if (tiles >= 1ll << 31) return hipErrorInvalidConfiguration;  // (of a result that no memory holds)
   hipLaunchKernelGGL((matmul_few<BF, S, HOW>), dim3((unsigned)(tiles < kMostBlocks ? tiles : kMostBlocks)), dim3(64 * S::WAVES), 0,
-                     s, a, (unsigned)tiles, (unsigned)((a.N + S::COLS - 1) / S::COLS));
+                     s, a, (unsigned)tiles, (unsigned)tiles_n);
   return hipGetLastError();
 }
 

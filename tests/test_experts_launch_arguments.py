@@ -1,0 +1,54 @@
+"""What the launches of the grouped and 4-bit products pass to their kernels at
+the ends of the documented ranges, on the CPU.  (tests/experts_dry_run.py)"""
+import re
+import shutil
+
+import pytest
+
+from dense_gemm_row_amd import gemm, w4
+from tests import experts_dry_run
+from tests.mx_dry_run import STAND_IN
+
+TOP = 2 ** 31 - 1
+F32, F16, BF16 = gemm.DTYPE_F32, gemm.DTYPE_F16, gemm.DTYPE_BF16
+O, X, W, Y, Q, S, Z = (i << 52 for i in range(1, 8))  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def dry(tmp_path_factory):
+    if shutil.which("g++") is None:
+        pytest.skip("needs g++")
+    first = '{"matmul_direct", "48"}'
+    assert first in STAND_IN
+    with pytest.MonkeyPatch.context() as m:  # (records the kernels' tiles and columns of tiles too)
+        m.setattr(experts_dry_run, "STAND_IN", STAND_IN.replace(first, first + ', {"matmul_few", "44"}'))
+        return experts_dry_run.compile_dry(str(tmp_path_factory.mktemp("dry")))
+
+
+def coded(group, K, N):
+    ng = -(-K // group)
+    ldq = -(-K // 32) * 16
+    return w4.GemmW4(Q, ldq, N * ldq, S, ng, N * ng, Z, ng, N * ng, group)
+
+
+def shape(launch):
+    """(k of a scale, blocks of 16 rows, waves along k, waves) of the kernel for few rows."""
+    gb, mb, nb, kw, waves = map(int, re.search(r"5ShapeILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)E", launch.name.decode()).groups())
+    assert nb == 1
+    return gb, mb, kw, waves
+
+
+@pytest.mark.parametrize("group", w4.GROUPS)
+@pytest.mark.parametrize("N", [TOP, TOP - 1, TOP - 31, TOP - 63, TOP - 127, TOP - 128])
+def test_columns_of_tiles_of_4_bit_products(dry, N, group):
+    """Two experts of a row each, and dense products: a tile's columns are
+    counted without leaving 31 bits."""
+    for call in [("gemm_w4_grouped", BF16, 2, 2, N, 32, O, X, 32, coded(group, 32, N), Y, N, 0, None, 0, None)] + [
+            ("gemm_w4_matmul", BF16, M, N, K, X, K, coded(group, K, N), Y, N, None, 0, None)
+            for M in (1, 16, 17, 40, 128) for K in (32, 256)]:
+        status, launches = dry(*call)
+        assert status == gemm.GEMM_OK and len(launches) == 1
+        _, mb, kw, waves = shape(launches[0])
+        rows = 2 if call[0] == "gemm_w4_grouped" else -(-call[2] // (16 * mb))
+        cols = -(-N // (16 * (waves // kw)))
+        assert launches[0].arg[1] == cols and launches[0].arg[0] == rows * cols
