@@ -40,7 +40,7 @@ namespace w4 {
 namespace {
 
 constexpr unsigned OOB = 0x80000000u;  // offset past every descriptor's range
-constexpr int64_t kMostBlocks = 1 << 22;
+constexpr int64_t kMostItems = 1ll << 31;  // work-items of a grid (the runtime takes fewer than 2^32); workgroups walk on from there
 constexpr int64_t kFar = 1 << 22;  // leading dimensions below it: a tile's rows and columns are within 31 bits of bytes
 
 template <class F, int... I>
@@ -481,8 +481,9 @@ hipError_t start(const MatmulArgs& a, hipStream_t s) {
   const int64_t tiles = tiles_of(a, S::ROWS, S::COLS), tiles_n = ((int64_t)a.N + S::COLS - 1) / S::COLS;
   if (tiles <= 0) return hipSuccess;
   if (tiles >= 1ll << 31) return hipErrorInvalidConfiguration;  // (of a result that no memory holds)
-  hipLaunchKernelGGL((matmul_few<BF, S, HOW>), dim3((unsigned)(tiles < kMostBlocks ? tiles : kMostBlocks)), dim3(64 * S::WAVES), 0,
-                     s, a, (unsigned)tiles, (unsigned)tiles_n);
+  constexpr int64_t threads = 64 * S::WAVES, most = kMostItems / threads;
+  hipLaunchKernelGGL((matmul_few<BF, S, HOW>), dim3((unsigned)(tiles < most ? tiles : most)), dim3((unsigned)threads), 0, s, a,
+                     (unsigned)tiles, (unsigned)tiles_n);
   return hipGetLastError();
 }
 

@@ -52,3 +52,16 @@ def test_columns_of_tiles_of_4_bit_products(dry, N, group):
         rows = 2 if call[0] == "gemm_w4_grouped" else -(-call[2] // (16 * mb))
         cols = -(-N // (16 * (waves // kw)))
         assert launches[0].arg[1] == cols and launches[0].arg[0] == rows * cols
+
+
+@pytest.mark.parametrize("group", w4.GROUPS)
+@pytest.mark.parametrize("N", [2 ** 28, 2 ** 28 + 1, 2 ** 30, TOP])
+def test_grids_of_4_bit_products_of_any_rows(dry, N, group):
+    """Fewer than 2^32 work-items, for workgroups of 8 and of 16 waves."""
+    sizes = set()
+    for M in (1, 33, 40, 48, 64, 128):
+        for K in (64, 128, 4096):
+            status, (one,) = dry("gemm_w4_matmul", BF16, M, N, K, X, K, coded(group, K, N), Y, N, None, 0, None)
+            assert status == gemm.GEMM_OK and one.grid[0] * one.block < 2 ** 32, (M, K, one.name, tuple(one.grid), one.block)
+            sizes.add(one.block)
+    assert sizes == {512, 1024}
