@@ -67,13 +67,14 @@ int64_t workspace_for(bool many, int64_t G, int64_t N, int64_t K) {
   const unsigned __int128 n = many ? (unsigned __int128)(uint64_t)G * (uint64_t)N * (uint64_t)(2 * row_values(K)) : 0;
   return n < kSpanLimit ? (int64_t)n : -1;
 }
-gemm_status_t check_workspace(const void* p, int64_t bytes, int64_t need, const CodedSpans& q, const Span& x, const Span& y) {
+gemm_status_t check_workspace(const void* p, int64_t bytes, int64_t need, const CodedSpans& q, const Span& x, const Span& y,
+                              const Span& offsets) {
   if (need < 0) return fail(GEMM_ERR_INVALID_ARG, "the dequantised weights' bytes reach 2^63");
   if (need == 0) return GEMM_OK;
   if (!p || bytes < need) return fail(GEMM_ERR_INVALID_ARG, "the workspace takes %lld bytes", (long long)need);
   if ((uintptr_t)p % 16 != 0) return fail(GEMM_ERR_INVALID_ARG, "workspace not 16-byte aligned");
   const Span k = span(p, 1, need, need);
-  if (overlap(k, x) || overlap(k, y) || q.meets(k)) return fail(GEMM_ERR_ALIAS, "workspace overlaps an operand");
+  if (overlap(k, x) || overlap(k, y) || overlap(k, offsets) || q.meets(k)) return fail(GEMM_ERR_ALIAS, "workspace overlaps an operand");
   return GEMM_OK;
 }
 
@@ -166,7 +167,7 @@ gemm_status_t gemm_w4_matmul(int32_t dtype, int64_t M, int64_t N, int64_t K, con
   if (overlap(y, x) || c.meets(y)) return fail(GEMM_ERR_ALIAS, "Y overlaps an operand");
   if (M == 0 || N == 0) return GEMM_OK;
   const int64_t need = gemm_w4_matmul_workspace_bytes(M, N, K);
-  if ((st = check_workspace(workspace, workspace_bytes, need, c, x, y)) != GEMM_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, need, c, x, y, Span{0, 0})) != GEMM_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!many_rows(M, 1, K))
     return launched(few_rows(dtype, q->group, args_of(q, X, ldx, Y, ldy, M, N, K, 1, nullptr, 0), s));
@@ -203,15 +204,15 @@ gemm_status_t gemm_w4_grouped(int32_t dtype, int64_t G, int64_t T, int64_t N, in
   gemm_status_t st;
   CodedSpans c;
   Span x, y;
+  const Span o = span(offsets, 1, 4 * (G + 1), 4 * (G + 1));
   if ((st = w4::check_sizes(N, K)) != GEMM_OK) return st;
   if ((st = check_dense("X", X, T, K, ldx, 2, &x)) != GEMM_OK) return st;
   if ((st = w4::check_coded(q, G, N, K, &c)) != GEMM_OK) return st;
   if ((st = check_dense("Y", Y, T, N, ldy, 2, &y)) != GEMM_OK) return st;
-  if (overlap(y, x) || c.meets(y) || overlap(y, span(offsets, 1, 4 * (G + 1), 4 * (G + 1))))
-    return fail(GEMM_ERR_ALIAS, "Y overlaps an operand");
+  if (overlap(y, x) || c.meets(y) || overlap(y, o)) return fail(GEMM_ERR_ALIAS, "Y overlaps an operand");
   if (T == 0 || N == 0) return GEMM_OK;
   const int64_t need = gemm_w4_grouped_workspace_bytes(G, T, N, K);
-  if ((st = check_workspace(workspace, workspace_bytes, need, c, x, y)) != GEMM_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, need, c, x, y, o)) != GEMM_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!many_rows(T, G, K))
     return launched(few_rows(dtype, q->group, args_of(q, X, ldx, Y, ldy, T, N, K, G, offsets, fill), s));

@@ -105,8 +105,8 @@ int64_t gemm_w4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * (X T x K, Y T x N; `offsets` and `fill` as in gemm_grouped_matmul).  Up to
  * GEMM_W4_ROWS rows a group on average (T <= GEMM_W4_ROWS * G) the codes are
  * read by the product itself, each group's codes once for every 16, 32 or 64 of
- * its rows; beyond, all G matrices are dequantised into
- * `workspace` and multiplied as gemm_grouped_matmul does.
+ * its rows; beyond, all G matrices are dequantised into `workspace`, which must
+ * not overlap `offsets` either, and multiplied as gemm_grouped_matmul does.
  */
 gemm_status_t gemm_w4_grouped(int32_t dtype, int64_t G, int64_t T, int64_t N, int64_t K, const int32_t *offsets,
                               const void *X, int64_t ldx, const gemm_w4_t *q, void *Y, int64_t ldy, int32_t fill,
