@@ -93,13 +93,13 @@ double tile_us(double tiles, int at_once, double fixed, double per_slice, double
 // groups of one row, 2048 x 1024, 18.6 and 31.6 us; 16 of 31, 1000 x 1000, 20.4 and
 // 12.0; 8 of 12, 4096 x 1024, 15.3 and 25.3; 64 of 16, 1024 x 2048, 85 and 64.)
 int tile_for(const MatmulArgs& a) {
-  const double slices = (a.K + 63) / 64, groups = a.T < a.G ? a.T : a.G, of_one = 2. * a.N * a.K / 5.2e6, read = groups * of_one;
+  const double slices = tiles_along(a.K, 64), groups = a.T < a.G ? a.T : a.G, of_one = 2. * a.N * a.K / 5.2e6, read = groups * of_one;
   auto us = [&](int side, int at_once, double fixed, double per_slice, double lone) {
     const double tiles = likely_tiles(a, side);
     return tile_us(tiles, at_once, fixed, tiles <= kCus ? lone : per_slice, slices);
   };
   const double m = a.T / 16. + 0.5 * groups, read16 = (m < a.T ? m : a.T) * of_one;
-  const double us16 = tile_us(m * ((a.N + 63) / 64), 256, 3., 0.2, slices);
+  const double us16 = tile_us(m * tiles_along(a.N, 64), 256, 3., 0.2, slices);
   const double us128 = alone(a) ? 4.8 + 0.34 * slices : us(128, 512, 5.5, 1.1, 0.66), us256 = us(256, 256, 13., 1.35, 1.35);
   if ((us16 > read16 ? us16 : read16) < (us128 > read ? us128 : read) && us16 < us256) return 16;
   return us256 < us128 ? 256 : 128;

@@ -340,7 +340,6 @@ __global__ void __launch_bounds__(THREADS, 2) wgrad_general(WgradArgs p, int64_t
 }
 
 dim3 grid_of(int64_t tiles) { return dim3((unsigned)(tiles < kMostBlocks ? tiles : kMostBlocks)); }
-int64_t tiles_along(int64_t n, int side) { return (n + side - 1) / side; }
 
 template <int DT, int CT, int SIDE>
 hipError_t on_tile(const MatmulArgs& a, hipStream_t s) {

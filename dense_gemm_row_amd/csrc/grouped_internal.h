@@ -44,14 +44,16 @@ hipError_t launch_pipe(const MatmulArgs& a, hipStream_t s);
 template <int DT, int CT, int SIDE>
 hipError_t launch_pipe(const WgradArgs& a, hipStream_t s);
 
+// Tiles of `side` along n.
+inline int64_t tiles_along(int64_t n, int side) { return (n + side - 1) / side; }
 // Tiles of `side` x `side` that are likely: a group ends in half a row tile on
 // average, and has one where it has a row.
 inline double likely_tiles(const MatmulArgs& a, int side) {
   const double some = a.T < a.G ? a.T : a.G, m = (double)a.T / side + 0.5 * some;
-  return (m > some ? m : some) * ((a.N + side - 1) / side);
+  return (m > some ? m : some) * tiles_along(a.N, side);
 }
 inline double likely_tiles(const WgradArgs& a, int side) {
-  return (double)a.G * ((a.K + side - 1) / side) * ((a.N + side - 1) / side);
+  return (double)a.G * tiles_along(a.K, side) * tiles_along(a.N, side);
 }
 // Whether the tiles of 128 x 128 do not have to share a CU (the product's with
 // some to spare: a second round costs more): then four LDS stages, three
