@@ -83,9 +83,11 @@ gemm_status_t gemm_w4_dequantize(int32_t dtype, int32_t s_dtype, int64_t N, int6
  * with scales of that type.  Up to GEMM_W4_ROWS rows, the codes enter the matrix
  * core as the whole numbers 16 + q (exact in both types), each group's sum is
  * accumulated in FP32, 16 + zero point times the sum of its activations is
- * taken off and the scale applied in FP32; the result is rounded once.  (So an
- * activation that is infinite gives NaN, not an infinity, and sums of a group's
- * activations have to stay below 2^123.)  With more rows the weights are
+ * taken off and the scale applied in FP32; the result is rounded once.  (Where
+ * these sums are not finite, for an infinite activation or one near the end of
+ * bfloat16's range, a result is taken from sum s (q - zero point) x in 64 bits
+ * instead: infinities and NaN are those of the definition, and such a result
+ * takes K / 32 steps of one thread.)  With more rows the weights are
  * dequantised first, rounded to dtype, into `workspace`
  * (gemm_w4_matmul_workspace_bytes bytes, 16-byte aligned, not overlapping the
  * operands; too small a one -> INVALID_ARG) and multiplied as gemm_*_bt does;
