@@ -104,12 +104,25 @@ def _result_dtype(dtype, operand):
     return dtype
 
 
+def _no_graph(name, instead):
+    """Refuses an operand whose gradient the result would lose."""
+    if mx._torch is None:
+        mx._load()
+    if mx._torch.is_grad_enabled():
+        raise RuntimeError(f"{name} records no graph, so an operand that requires a gradient would get none: {instead}call it "
+                           "under torch.no_grad() or with detached operands")
+
+
 def matmul(x, w, offsets, transposed: bool = False, out=None, out_dtype=None, stream=None):
     """y[t] = x[t] @ w[g] for the rows t of every group g, rows offsets[g] to
     offsets[g + 1] - 1 of x (T x K).  w is groups x K x N, or with
     ``transposed`` groups x N x K (y[t] = x[t] @ w[g].T), of x's type.  The
     result (T x N) has x's type or float32 (out_dtype).  Rows of no group are
-    zero in a new result; in ``out`` they stay as they are."""
+    zero in a new result; in ``out`` they stay as they are.  No graph is
+    recorded: where one would be (an operand requires a gradient and grad mode
+    is on) the call is refused; `linear` records one."""
+    if x.requires_grad or w.requires_grad:
+        _no_graph("grouped.matmul", "use grouped.linear, or ")
     dtype, T, K, ldx = mx._dense(x, "x")
     w_dtype, G, rows, cols, ldw, stride_w = _stack(w, "w")
     N, inner = (rows, cols) if transposed else (cols, rows)

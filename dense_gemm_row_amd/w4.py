@@ -259,9 +259,11 @@ def dequantize(q: W4Tensor, dtype=None, out=None, stream=None):
     return out
 
 
-def _operands(x, q, dims, out, stream):
+def _operands(name, x, q, dims, out, stream):
     """The checks that both products share: (library dtype, rows, K, ldx, N,
     launch, out, ldy)."""
+    if isinstance(q, W4Tensor) and (x.requires_grad or q.scales.requires_grad):
+        grouped._no_graph(name, "")
     _coded(q, "q", dims)
     dtype, rows, K, ldx = mx._dense(x, "x")
     if x.dtype != q.scales.dtype:
@@ -285,8 +287,9 @@ def matmul(x, q: W4Tensor, out=None, stream=None):
     """x @ w.T for 4-bit weights q (N x K) and x (M x K) of the scales' type,
     which is the result's.  Up to 128 rows the codes are multiplied as they
     are; more rows multiply dequantised weights, rounded to that type, through
-    a workspace of 2 N K bytes.  (For serving: no gradients.)"""
-    dtype, M, K, ldx, N, on, out, ldy = _operands(x, q, 2, out, stream)
+    a workspace of 2 N K bytes.  (For serving: no graph is recorded, and the
+    call is refused where one would be, as by ``grouped.matmul``.)"""
+    dtype, M, K, ldx, N, on, out, ldy = _operands("w4.matmul", x, q, 2, out, stream)
     need = 0 if M <= ROWS else lib().gemm_w4_matmul_workspace_bytes(M, N, K)
     ws = on.empty(need, mx._torch.uint8) if need > 0 else None
     grouped._call(lib(), "gemm_w4_matmul", x.get_device(), dtype, M, N, K, x.data_ptr(), ldx, ctypes.byref(q._desc()),
@@ -299,9 +302,10 @@ def grouped_matmul(x, q: W4Tensor, offsets, out=None, stream=None):
     offsets[g + 1] - 1 of x (T x K), and a stack q of 4-bit weights (experts x
     N x K).  Rows of no group are zero in a new result; in ``out`` they stay as
     they are.  (Above 128 rows an expert on average all experts' weights are
-    dequantised first.  For serving: no gradients.)"""
+    dequantised first.  For serving: no graph is recorded, and the call is
+    refused where one would be, as by ``grouped.matmul``.)"""
     fill = out is None
-    dtype, T, K, ldx, N, on, out, ldy = _operands(x, q, 3, out, stream)
+    dtype, T, K, ldx, N, on, out, ldy = _operands("w4.grouped_matmul", x, q, 3, out, stream)
     G = q.codes.shape[0]
     at = grouped._offsets(offsets, G, x)
     need = 0 if T <= ROWS * G else lib().gemm_w4_grouped_workspace_bytes(G, T, N, K)
