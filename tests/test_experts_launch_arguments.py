@@ -2,11 +2,13 @@
 the ends of the documented ranges, on the CPU.  (tests/experts_dry_run.py)"""
 import re
 import shutil
+import subprocess
 
 import pytest
 
 from dense_gemm_row_amd import gemm, w4
 from tests import experts_dry_run
+from tests.experts4_sizes import READS, SHAPES
 from tests.mx_dry_run import STAND_IN
 
 TOP = 2 ** 31 - 1
@@ -31,11 +33,20 @@ def coded(group, K, N):
     return w4.GemmW4(Q, ldq, N * ldq, S, ng, N * ng, Z, ng, N * ng, group)
 
 
-def shape(launch):
+def shape_of(name):
     """(k of a scale, blocks of 16 rows, waves along k, waves) of the kernel for few rows."""
-    gb, mb, nb, kw, waves = map(int, re.search(r"5ShapeILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)E", launch.name.decode()).groups())
+    gb, mb, nb, kw, waves = map(int, re.search(r"5ShapeILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)E", name).groups())
     assert nb == 1
     return gb, mb, kw, waves
+
+
+def shape(launch):
+    return shape_of(launch.name.decode())
+
+
+def kernel_names(dry):
+    """Every kernel that the library registers."""
+    return subprocess.run(["strings", "-n", "20", dry.lib._name], check=True, capture_output=True, text=True).stdout.split()
 
 
 @pytest.mark.parametrize("group", w4.GROUPS)
@@ -65,3 +76,27 @@ def test_grids_of_4_bit_products_of_any_rows(dry, N, group):
             assert status == gemm.GEMM_OK and one.grid[0] * one.block < 2 ** 32, (M, K, one.name, tuple(one.grid), one.block)
             sizes.add(one.block)
     assert sizes == {512, 1024}
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group", w4.GROUPS)
+@pytest.mark.parametrize("want", SHAPES, ids=str)
+def test_shapes_of_4_bit_products(dry, want, group, dtype):
+    for rows, N, offsets in SHAPES[want]:
+        for reads, ks in READS.items():
+            for K in ks:
+                q = coded(group, K, N)
+                if offsets is None:
+                    status, (one,) = dry("gemm_w4_matmul", dtype, rows, N, K, X, K, q, Y, N, None, 0, None)
+                else:
+                    status, (one,) = dry("gemm_w4_grouped", dtype, len(offsets) - 1, rows, N, K, O, X, K, q, Y, N, 1, None, 0, None)
+                got = re.search(r"5ReadsE(\d)E", one.name.decode()).group(1)
+                assert status == gemm.GEMM_OK and shape(one) == (group, *want) and int(got) == reads, (rows, N, K, one.name)
+
+
+def test_every_shape_has_sizes(dry):
+    """The kernels that are built, but for the one by element (blocks of one,
+    a wave along k), are those of the table."""
+    built = {(shape_of(n), int(re.search(r"5ReadsE(\d)E", n).group(1))) for n in kernel_names(dry) if "5Shape" in n}
+    assert built == {((group, *s), reads) for s in SHAPES for reads in READS for group in w4.GROUPS} | {
+        ((group, 1, 1, 8), 0) for group in w4.GROUPS}
