@@ -1,5 +1,5 @@
-// Index arithmetic of the grouped products that decides which rows, tiles and
-// workgroups there are: plain integers, the same on the host, on the device
+// Index arithmetic of the grouped and 4-bit products that decides which rows,
+// tiles and workgroups there are, and where operands of any alignment are read: plain integers, the same on the host, on the device
 // and in a CPU test that includes this header alone.
 #pragma once
 
@@ -33,6 +33,31 @@ GROUPED_HD int segment_tiles(int rows, int bm) { return (int)(((int64_t)rows + b
 GROUPED_HD int64_t most_tiles(int64_t T, int64_t G, int fill, int bm) {
   const int64_t S = G + (fill ? 2 : 0), n = (T + S * (bm - 1)) / bm;
   return S == 0 ? 0 : n < T ? n : T;
+}
+
+// Reads in whole pieces of `per` values wherever a row ends: by how many values
+// the piece that has `left` values ahead of the row's end begins early, so that
+// it ends there (the row has a whole piece; what it does not need is shifted out).
+template <class I>
+GROUPED_HD int piece_early(I left, int per) { return left >= per ? 0 : per - (int)left; }
+
+// The same by position: where `width` values from n on are read in a row of
+// `count` >= width.
+GROUPED_HD int piece_start(int n, int count, int width) { return n < count - width ? n : count - width; }
+
+// The byte of a row of codes where the 16 bytes with k are (k a multiple of 32;
+// `padded` is the row's k, whole 32): past the row's end, the row's first ones.
+GROUPED_HD int code_byte(int k, int padded) { return k < padded ? k / 2 : 0; }
+
+// The first k of the i-th span that wave row `part` of PARTS takes, `spans`
+// of them from the turn-th on; from `spans` on, a whole span past the end (`past`),
+// so that a lane's whole 32 k of it are there or not.
+template <int SPAN>
+GROUPED_HD int past_spans(int K) { return (K + SPAN - 1) / SPAN * SPAN; }
+template <int PARTS, int SPAN>
+GROUPED_HD int span_start(int i, int spans, int turn, int part, int past) {
+  const int j = i + turn < spans ? i + turn : i + turn - spans;
+  return i < spans ? (part + j * PARTS) * SPAN : past;
 }
 
 }  // namespace grouped

@@ -80,8 +80,8 @@ struct Panel {
     tiny = ACROSS ? o.total < PER : K < PER;  // (no whole piece in a row)
     if constexpr (ACROSS) {
       first = row0();
-      const int n = PER * chunk(), last = rows - PER;
-      if (!tiny) cut = n > last ? n - last : 0;
+      const int n = PER * chunk();
+      if (!tiny) cut = piece_early(rows - n, PER);
       at[0] = o.at + row0() * ld + (n - cut);
     } else {
       first = PER * chunk();
@@ -110,7 +110,7 @@ struct Panel {
           for (int u = 0; u < PER; ++u) e[u] = (ACROSS ? PER * chunk() + u < rows : u < left) ? p[u] : (T)0.f;
           __builtin_memcpy(&v[i], e, 16);
         } else {
-          const int gone = ACROSS || left >= PER ? 0 : PER - (int)left;
+          const int gone = ACROSS ? 0 : piece_early(left, PER);
           __builtin_memcpy(&v[i], p - gone, 16);
           v[i] = without(v[i], gone, ES);
         }
@@ -221,6 +221,7 @@ __device__ __forceinline__ void tile_sums(const Operand<typename TypeOf<DT>::typ
   b.store(lb[0], rb[0]);
   fetch(DEPTH, EDGE, R0);
   int i = 0;
+  static_assert(2 + DEPTH <= 4, "the second step's fetch is of a whole slice");
   for (; i + 4 < whole; i += 2) {
     step(i, R0, WHOLE);
     step(i + 1, R1, WHOLE);

@@ -300,22 +300,21 @@ __global__ void __launch_bounds__(64 * S::WAVES) matmul_few(MatmulArgs p, unsign
 #pragma unroll
           for (int h = 0; h < SPAN / 128; ++h) {
             const int k = k0 + 128 * h + 32 * q;  // (the lane's piece is a whole 32 k, all of it there or none)
-            const unsigned off = q_at[j] + (unsigned)(k < padded ? k / 2 : 0);
+            const unsigned off = q_at[j] + (unsigned)grouped::code_byte(k, padded);
             __builtin_memcpy(c.w[j][h], __builtin_assume_aligned(codes0 + off, 16), 16);
           }
-          const int i = k0 / GB < ng - GROUPS ? k0 / GB : ng - GROUPS;
+          const int i = grouped::piece_start(k0 / GB, ng, GROUPS);
           words_at<2 * GROUPS>((const uint8_t*)scales0 + (s_at[j] + (unsigned)(2 * i)), c.s[j]);
           words_at<GROUPS>(zeros0 + (z_at[j] + (unsigned)i), c.z[j]);
         } else if (k0 < K) {
 #pragma unroll
           for (int h = 0; h < SPAN / 128; ++h) {
-            int k = k0 + 128 * h + 32 * q;
-            if (k >= padded) k = 0;
-            __builtin_memcpy(c.w[j][h], __builtin_assume_aligned(codes0 + col[j] * p.ldq + k / 2, 16), 16);
+            const int at = grouped::code_byte(k0 + 128 * h + 32 * q, padded);
+            __builtin_memcpy(c.w[j][h], __builtin_assume_aligned(codes0 + col[j] * p.ldq + at, 16), 16);
           }
 #pragma unroll
           for (int h = 0; h < GROUPS; ++h) {
-            const int i = k0 / GB + h < ng ? k0 / GB + h : ng - 1;
+            const int i = grouped::piece_start(k0 / GB + h, ng, 1);
             c.s[j][h / 2] = (h % 2 ? c.s[j][h / 2] : 0u) | (unsigned)scales0[col[j] * p.lds + i] << (16 * (h % 2));
             c.z[j][h / 4] = (h % 4 ? c.z[j][h / 4] : 0u) | (p.zeros ? (unsigned)zeros0[col[j] * p.ldz + i] : 0u) << (8 * (h % 4));
           }
@@ -330,7 +329,7 @@ __global__ void __launch_bounds__(64 * S::WAVES) matmul_few(MatmulArgs p, unsign
           const unsigned off = k0 + xk[i] < K ? x_at[i] + 2 * k0 : OOB;
           buffer_words<4>(from_x, off, reinterpret_cast<unsigned(&)[4]>(xv[i]));
         } else if (pieces) {
-          const int k = k0 + xk[i] < p.K - 8 ? k0 + xk[i] : p.K - 8;  // (K may be 0)
+          const int k = grouped::piece_start(k0 + xk[i], p.K, 8);  // (K may be 0)
           __builtin_memcpy(&xv[i], (const uint8_t*)x0 + (x_at[i] + (unsigned)(2 * k)), 16);
         } else {
           uint16_t e[8];
@@ -436,12 +435,9 @@ __global__ void __launch_bounds__(64 * S::WAVES) matmul_few(MatmulArgs p, unsign
     constexpr int DEPTH = S::SHARED && S::WAVES == 8 ? 4 : 2;  // (16 waves hide as much with half the registers)
     Codes<S> ring[DEPTH];
     const int spans = ((K + SPAN - 1) / SPAN + KW - 1) / KW;
-    const int none = (K + SPAN - 1) / SPAN * SPAN;  // (a whole span past the end, so that a lane's 32 k are there or not)
+    const int past = grouped::past_spans<SPAN>(K);
     const int turn = spans > 0 ? (int)(b % tiles_n % (unsigned)spans) : 0;
-    auto at = [&](int i) __attribute__((always_inline)) {
-      const int j = i + turn < spans ? i + turn : i + turn - spans;
-      return i < spans ? (kw + j * KW) * SPAN : none;
-    };
+    auto at = [&](int i) __attribute__((always_inline)) { return grouped::span_start<KW, SPAN>(i, spans, turn, kw, past); };
     // (In the order of the spans everywhere: the waits count on it.)
     auto fetch = [&](int i, Codes<S>& c) __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
