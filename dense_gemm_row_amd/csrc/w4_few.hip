@@ -172,8 +172,9 @@ __device__ __forceinline__ void without(unsigned (&w)[N], int n) {
 // of an infinite activation are infinities whose difference is NaN, and those of
 // a finite one from 2^123 on may leave FP32 where their difference would not.
 // (Such a result alone pays for it, and NaN ends it: 33 rows, 4096 x 11008, 20.5
-// us, 102 with one infinite activation, 21.1 with a NaN; in all: 60.2 and 60.8 us
-// of 64 experts of 2048 x 2048, 512 rows, without and with this check.)
+// us, 102 with one infinite activation, 21.1 with a NaN.  All others pay for the
+// check: 64 rows 24.8 and 25.0 us without and with it; 64 experts of 2048 x 2048, 512
+// rows, 46.2 and 46.4.)
 template <bool BF, int GB>
 __device__ __forceinline__ float defined(int g, int64_t m, int64_t n, int K) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -207,6 +208,7 @@ __device__ __forceinline__ float defined(int g, int64_t m, int64_t n, int K) {
     }
     if (sum != sum) break;
   }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0) (see the results' loop)
   return (float)sum;
 #else
   return 0.f;
@@ -484,6 +486,10 @@ __global__ void __launch_bounds__(64 * S::WAVES) matmul_few(MatmulArgs p, unsign
         for (int e = 0; e < 4; ++e)
           sums[(kw * S::ROWS + 16 * i + 4 * q + e) * S::COLS + 16 * (NB * nw + j) + r] = acc[j][i][e];
     barrier();
+    // vmcnt(0): with loads on their way, these or those of `defined`, the compiler
+    // waits in the loop, and so for every result's store (64 rows, 4096 x 11008:
+    // 25.6 us, with this wait 25.0).
+    __builtin_amdgcn_s_waitcnt(0x0f70);
     for (int i = tid; i < S::ROWS * S::COLS; i += 64 * S::WAVES) {
       const int m = i / S::COLS, col = i % S::COLS;
       if (m >= t.rows || n0 + col >= p.N) continue;
