@@ -113,6 +113,12 @@ def _no_graph(name, instead):
                            "under torch.no_grad() or with detached operands")
 
 
+def _written(*tensors):
+    """Tells autograd that a caller's tensors were written, as torch's own
+    operators do: a graph that has saved one of them refuses its backward pass."""
+    mx._torch.autograd.graph.increment_version(tensors)
+
+
 def matmul(x, w, offsets, transposed: bool = False, out=None, out_dtype=None, stream=None):
     """y[t] = x[t] @ w[g] for the rows t of every group g, rows offsets[g] to
     offsets[g + 1] - 1 of x (T x K).  w is groups x K x N, or with
@@ -143,6 +149,8 @@ def matmul(x, w, offsets, transposed: bool = False, out=None, out_dtype=None, st
     mx._same_device(out, x)
     _call(lib(), "gemm_grouped_matmul", x.get_device(), dtype, c_dtype, 1 if transposed else 0, G, T, N, K, at, x.data_ptr(),
           ldx, w.data_ptr(), ldw, stride_w, out.data_ptr(), ldy, 1 if fill else 0, on.handle)
+    if not fill:
+        _written(out)
     return out
 
 
@@ -163,7 +171,8 @@ def weight_grad(x, dy, offsets, out=None, out_dtype=None, alpha: float = 1.0, be
     G = offsets.shape[0] - 1
     at = _offsets(offsets, G, x)
     on = mx._Launch(x, stream)
-    if out is None:
+    given = out is not None
+    if not given:
         if beta != 0.0:
             raise ValueError("beta needs out")
         out = on.empty((G, K, N), _result_dtype(out_dtype or mx._torch.float32, x.dtype))
@@ -174,6 +183,8 @@ def weight_grad(x, dy, offsets, out=None, out_dtype=None, alpha: float = 1.0, be
     mx._same_device(out, x)
     _call(lib(), "gemm_grouped_wgrad", x.get_device(), dtype, c_dtype, G, T, K, N, at, x.data_ptr(), ldx, dy.data_ptr(),
           ldy, out.data_ptr(), ldw, stride_w, alpha, beta, on.handle)
+    if given:
+        _written(out)
     return out
 
 

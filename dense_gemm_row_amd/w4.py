@@ -214,7 +214,8 @@ def quantize(w, group: int = 128, zeros: bool = True, transposed: bool = False, 
     torch = mx._torch
     N, K = (cols, rows) if transposed else (rows, cols)
     shape = (w.shape[0], N, K) if stack else (N, K)
-    if out is None:
+    given = out is not None
+    if not given:
         kind = scale_dtype or (torch.bfloat16 if w.dtype == torch.float32 else w.dtype)
         if kind not in (torch.float16, torch.bfloat16):
             raise TypeError("scale_dtype must be float16 or bfloat16")
@@ -234,6 +235,8 @@ def quantize(w, group: int = 128, zeros: bool = True, transposed: bool = False, 
         m, q = (w[e], out[e]) if stack else (w, out)
         grouped._call(lib(), "gemm_w4_quantize", w.get_device(), dtype, mx._DTYPES[q.scales.dtype], 1 if transposed else 0, N, K,
                       m.data_ptr(), ldx, ctypes.byref(q._desc()), on.handle)
+    if given:
+        grouped._written(*(t for t in (out.codes, out.scales, out.zeros) if t is not None))
     return out
 
 
@@ -244,7 +247,8 @@ def dequantize(q: W4Tensor, dtype=None, out=None, stream=None):
     torch = mx._torch
     stack = q.codes.dim() == 3
     on = mx._Launch(q.codes, stream)
-    if out is None:
+    given = out is not None
+    if not given:
         out = on.empty(q.shape, mx._out_dtype(dtype, q.scales.dtype, "dtype"))
     elif tuple(out.shape) != q.shape or (dtype is not None and out.dtype != dtype):
         raise ValueError("out has the wrong shape or dtype")
@@ -256,6 +260,8 @@ def dequantize(q: W4Tensor, dtype=None, out=None, stream=None):
         x_dtype, N, K, ldx = mx._dense(x, "out")
         grouped._call(lib(), "gemm_w4_dequantize", q.codes.get_device(), x_dtype, mx._DTYPES[q.scales.dtype], N, K,
                       ctypes.byref(one._desc()), x.data_ptr(), ldx, on.handle)
+    if given:
+        grouped._written(out)
     return out
 
 
@@ -289,11 +295,14 @@ def matmul(x, q: W4Tensor, out=None, stream=None):
     are; more rows multiply dequantised weights, rounded to that type, through
     a workspace of 2 N K bytes.  (For serving: no graph is recorded, and the
     call is refused where one would be, as by ``grouped.matmul``.)"""
+    given = out is not None
     dtype, M, K, ldx, N, on, out, ldy = _operands("w4.matmul", x, q, 2, out, stream)
     need = 0 if M <= ROWS else lib().gemm_w4_matmul_workspace_bytes(M, N, K)
     ws = on.empty(need, mx._torch.uint8) if need > 0 else None
     grouped._call(lib(), "gemm_w4_matmul", x.get_device(), dtype, M, N, K, x.data_ptr(), ldx, ctypes.byref(q._desc()),
                   out.data_ptr(), ldy, ws.data_ptr() if ws is not None else None, max(need, 0), on.handle)
+    if given:
+        grouped._written(out)
     return out
 
 
@@ -312,4 +321,6 @@ def grouped_matmul(x, q: W4Tensor, offsets, out=None, stream=None):
     ws = on.empty(need, mx._torch.uint8) if need > 0 else None
     grouped._call(lib(), "gemm_w4_grouped", x.get_device(), dtype, G, T, N, K, at, x.data_ptr(), ldx, ctypes.byref(q._desc()),
                   out.data_ptr(), ldy, 1 if fill else 0, ws.data_ptr() if ws is not None else None, max(need, 0), on.handle)
+    if not fill:
+        grouped._written(out)
     return out
