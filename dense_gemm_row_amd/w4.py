@@ -170,6 +170,14 @@ def _coded(q, name, dims):
         raise ValueError(f"{name} must be " + ("one matrix (N x K)" if dims == 2 else "a stack of matrices (experts x N x K)"))
 
 
+def _apart(t, name):
+    """Refuses a stack of results two of which share memory (an expanded one)."""
+    groups, rows, cols = t.shape
+    (near, n), (far, m) = sorted(((t.stride(0), groups), (t.stride(1), rows)))
+    if t.numel() > 0 and ((n > 1 and near < cols) or (m > 1 and far < (n - 1) * near + cols)):
+        raise ValueError(f"{name}: results of two experts or rows overlap")
+
+
 def empty(shape, group: int, device, scale_dtype=None, zeros: bool = True) -> W4Tensor:
     """Uninitialised 4-bit weights of shape (N, K) or (experts, N, K), scale
     rows of whole 256 k."""
@@ -230,6 +238,10 @@ def quantize(w, group: int = 128, zeros: bool = True, transposed: bool = False, 
         mx._same_device(w, out)
         if out.shape != shape:
             raise ValueError(f"out has shape {out.shape}, not {shape}")
+        if stack:
+            for part in (out.codes, out.scales, out.zeros):
+                if part is not None:
+                    _apart(part, "out")
         on = mx._Launch(first, stream)
     for e in range(shape[0] if stack else 1):
         m, q = (w[e], out[e]) if stack else (w, out)
@@ -255,6 +267,8 @@ def dequantize(q: W4Tensor, dtype=None, out=None, stream=None):
     if not isinstance(out, torch.Tensor) or not out.is_cuda:
         raise ValueError("out must be a GPU tensor")
     mx._same_device(q, out)
+    if stack and given:
+        _apart(out, "out")
     for e in range(q.shape[0] if stack else 1):
         one, x = (q[e], out[e]) if stack else (q, out)
         x_dtype, N, K, ldx = mx._dense(x, "out")

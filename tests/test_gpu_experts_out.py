@@ -51,3 +51,18 @@ def test_coded_results(zeros):
         before = [t._version for t in parts]
         assert w4.quantize(w, out=q) is q
         assert all(t._version > b for t, b in zip(parts, before))
+
+
+def test_stacks_of_results_that_overlap_are_refused():
+    w = ones(2, 32, 64)
+    q = w4.quantize(w, 32)
+    same = w4.W4Tensor(q.codes[:1].expand(2, 32, 32), q.scales, q.zeros, 64, 32)
+    scales = w4.W4Tensor(q.codes, q.scales[:1].expand(2, 32, 2), q.zeros, 64, 32)
+    zeros = w4.W4Tensor(q.codes, q.scales, q.zeros[:1].expand(2, 32, 2), 64, 32)
+    for out in (same, scales, zeros):
+        with pytest.raises(ValueError, match="overlap"):
+            w4.quantize(w, out=out)
+    with pytest.raises(ValueError, match="overlap"):
+        w4.dequantize(q, out=ones(32, 64).expand(2, 32, 64))
+    for out in (ones(32, 2, 64).transpose(0, 1), ones(2, 32, 70)[..., :64]):  # apart
+        assert torch.equal(w4.dequantize(q, out=out), w)
