@@ -23,8 +23,8 @@ gemm_status_t check_sizes(int64_t G, int64_t T, int64_t K, int64_t N, const int3
   return GEMM_OK;
 }
 
-// G matrices of rows x cols, `stride` elements apart; `apart`: they must not
-// overlap (an output's).
+// G matrices of rows x cols, `stride` elements apart; `apart`: they must lie one
+// behind another (an output's).
 gemm_status_t check_stack(const char* name, const void* p, int64_t G, int64_t rows, int64_t cols, int64_t ld, int64_t stride,
                           int64_t es, bool apart, Span* out) {
   Span one;
@@ -35,7 +35,7 @@ gemm_status_t check_stack(const char* name, const void* p, int64_t G, int64_t ro
   if (one.bytes == 0 || G <= 1) return GEMM_OK;
   if (stride >= (int64_t)(kSpanLimit >> 3)) return fail(GEMM_ERR_INVALID_ARG, "%s: byte range reaches 2^63", name);
   if (apart && (unsigned __int128)(uint64_t)stride * (unsigned)es < one.bytes)
-    return fail(GEMM_ERR_INVALID_ARG, "%s: the matrices of two groups overlap", name);
+    return fail(GEMM_ERR_INVALID_ARG, "%s: the matrices of two groups overlap, or lie between one another's rows", name);
   out->bytes += (unsigned __int128)(uint64_t)(G - 1) * (uint64_t)(stride * es);
   if (out->bytes >= kSpanLimit) return fail(GEMM_ERR_INVALID_ARG, "%s: byte range reaches 2^63", name);
   return GEMM_OK;

@@ -22,9 +22,9 @@
 //    scale are two fused operations a value.  A result that is not finite then is
 //    taken from the definition instead (`defined`).
 // Bound by the latency of its loads where there are few tiles (4096 x 4096, one
-// row: 6.8 us, 1.3 TB/s), by instructions and waits for loads where there are
-// many (64 experts of 2048 x 2048, a row each: 27.6 us, 4.9 TB/s; 512 rows: 54
-// us).
+// row: 7.2 us, 1.2 TB/s), by instructions and waits for loads where there are
+// many (64 experts of 2048 x 2048, groups of 128: a row each 42 us, 3.4 TB/s; 512 rows
+// as a router deals them 49, groups of 32 58 to 60).
 // One file for every combination of W4_TYPE (type of the activations) and
 // W4_GROUP (k of a scale): compiled once for each.
 #if !defined(W4_TYPE) || !defined(W4_GROUP)
@@ -507,9 +507,11 @@ __global__ void __launch_bounds__(64 * S::WAVES) matmul_few(MatmulArgs p, unsign
 // eight k, and a tile's rows and columns are within 31 bits of bytes.  WHOLE: X
 // in aligned 16-byte pieces besides, a span's scales and zero points as one
 // aligned load each, all of them there (a load that is partly past a
-// descriptor's range gives zeros).  (4096 x 11008, groups of 64, 33 rows: 22.9 us
-// WHOLE, 25.5 as SPANS; 64 experts of 2048 x 2048, groups of 32, 512 rows: 60.8
-// and 69.4.  K 4095, one row of 4096 columns: 13.6 us SPANS, 29.3 by element.)
+// descriptor's range gives zeros).  (WHOLE, as SPANS and as ANY, one wave along k:
+// 4096 x 11008, groups of 64, 33 rows 22.0, 22.6 and 84 us; 64 rows, groups of 128
+// 26.7, 27.5 and 57; 64 experts of 2048 x 2048, 512 rows 49, 56 and 69, groups of 32
+// 59, 64 and 217.  K 4095, one row of 4096 columns: 11.0 us SPANS, 38 ANY; 16 rows,
+// which begin on 2 bytes: 30.3 and 38.5, of K 4096 10.)
 template <class S>
 Reads reads_of(const MatmulArgs& a) {
   constexpr int64_t g = S::GROUPS;
@@ -544,7 +546,7 @@ hipError_t along(const MatmulArgs& a, int kw, hipStream_t s) {
   }
   if (kw >= 4) return start<BF, Shape<GB, MB, 1, 4>, HOW>(a, s);
   // (12 KB of X do not split over eight waves along the columns: four, and four
-  // along k.  M 33, 4096 x 11008: 20.6 us, 23.3 with two along k; with one or two
+  // along k.  M 33, 4096 x 11008: 19.0 us, 23.3 with two along k; with one or two
   // blocks of rows 16 waves gain nothing: M 1, 4096 x 4096, 9.0 us and 6.8 with 8.)
   if constexpr (MB == 3) return start<BF, Shape<GB, MB, 1, 4, 16>, HOW>(a, s);
   else return kw == 1 ? start<BF, Shape<GB, MB, 1, 1>, HOW>(a, s) : start<BF, Shape<GB, MB, 1, 2>, HOW>(a, s);
@@ -580,8 +582,14 @@ hipError_t launch_few(const MatmulArgs& a, hipStream_t s) {
     return kw;
   };
   // More rows a tile read fewer codes and more of X at once (M 64: 4096 x 4096
-  // 14.1 us on 32 rows, 18.9 on 64; 4096 x 11008 30.2 and 24.7.  M 33, 4096 x
-  // 11008: 20.6 us on 48 rows, 24.5 on 64).
+  // 14.1 us on 32 rows, 18.9 on 64; 4096 x 11008 30.2 and 24.7).  48 and 64 rows,
+  // dense: M 33, 40 and 48, 4096 x 6144 16.2, 15.4 and 15.7 us on 48 and 19.3, 18.8
+  // and 19.2 on 64; 4096 x 11008 19.5, 19.5 and 19.8 against 24.2, 24.3 and 24.5; 4096
+  // x 22016 36.9, 37.2 and 37.7 against 39.1, 39.2 and 39.6; groups of 32 alike.
+  // Experts: their rows differ, so that tiles of 48 are half empty where 64 were,
+  // only more of them: 1280 rows, 32 of 2048 x 2048, 66.4 and 64.9 us, groups of 32
+  // 81.6 and 64.9; 384 rows evenly to 8 of 2048 x 4096 27.5 and 24.0 (but 288 rows
+  // unevenly to 8 of 4096 x 4096 56.3 and 76.8).
   if (rows <= (a.offsets ? 16 : 32)) return on_rows<BF, GB, 1>(a, along_k(16), s);
   if (rows <= 32 || likely(64, 4) < 160) return on_rows<BF, GB, 2>(a, along_k(32), s);
   if (rows <= 48 && !a.offsets) return on_rows<BF, GB, 3>(a, along_k(48), s);

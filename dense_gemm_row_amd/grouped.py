@@ -158,7 +158,8 @@ def weight_grad(x, dy, offsets, out=None, out_dtype=None, alpha: float = 1.0, be
     """dw[g] = alpha * x_g.T @ dy_g + beta * out[g] for every group's rows of
     x (T x K) and dy (T x N), of one type: groups x K x N, float32 unless out
     or out_dtype says x's type.  A group without rows has zeros (beta = 1: out
-    as it is); beta = 1 accumulates over micro-batches."""
+    as it is); beta = 1 accumulates over micro-batches.  The matrices of out lie
+    one behind another (out.stride(0) at least a matrix's extent)."""
     dtype, T, K, ldx = mx._dense(x, "x")
     y_dtype, rows, N, ldy = mx._dense(dy, "dy")
     if y_dtype != dtype:

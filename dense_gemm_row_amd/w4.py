@@ -89,9 +89,10 @@ class W4Tensor:
     = K values a row, ``group`` (32, 64 or 128) of them to a scale.  With a
     leading dimension more they are a stack of matrices, one an expert.  All
     may be views with larger strides, rows contiguous; codes need 16-byte
-    alignment and strides of multiples of 16.  (Products of few rows are some
-    10 % faster where K is whole 256 k and rows of x, scales and zero points
-    begin aligned to 16 bytes and to 256 k's.)"""
+    alignment and strides of multiples of 16.  (Products of few rows are
+    fastest where K is whole 256 k and rows of x, scales and zero points begin
+    aligned to 16 bytes and to 256 k's; with an odd K, or rows of x that begin
+    on 2 bytes, some take three times as long: see include/gemm_w4.h.)"""
     __slots__ = ("codes", "scales", "zeros", "cols", "group")
 
     def __init__(self, codes, scales, zeros, cols: int, group: int = 128):
@@ -306,8 +307,8 @@ def _operands(name, x, q, dims, out, stream):
 def matmul(x, q: W4Tensor, out=None, stream=None):
     """x @ w.T for 4-bit weights q (N x K) and x (M x K) of the scales' type,
     which is the result's.  Up to 128 rows the codes are multiplied as they
-    are; more rows multiply dequantised weights, rounded to that type, through
-    a workspace of 2 N K bytes.  (For serving: no graph is recorded, and the
+    are; more rows multiply dequantised weights, rounded to that type (results
+    are off by about a third more), through a workspace of 2 N K bytes.  (For serving: no graph is recorded, and the
     call is refused where one would be, as by ``grouped.matmul``.)"""
     given = out is not None
     dtype, M, K, ldx, N, on, out, ldy = _operands("w4.matmul", x, q, 2, out, stream)
@@ -325,7 +326,7 @@ def grouped_matmul(x, q: W4Tensor, offsets, out=None, stream=None):
     offsets[g + 1] - 1 of x (T x K), and a stack q of 4-bit weights (experts x
     N x K).  Rows of no group are zero in a new result; in ``out`` they stay as
     they are.  (Above 128 rows an expert on average all experts' weights are
-    dequantised first.  For serving: no graph is recorded, and the call is
+    dequantised first, rounded to that type as in `matmul`.  For serving: no graph is recorded, and the call is
     refused where one would be, as by ``grouped.matmul``.)"""
     fill = out is None
     dtype, T, K, ldx, N, on, out, ldy = _operands("w4.grouped_matmul", x, q, 3, out, stream)

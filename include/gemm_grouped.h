@@ -25,7 +25,8 @@
  * the other rows' values.
  * T, N and K are 0 .. 2^31-1, G is 0 .. 65535.  Errors:
  *   a size outside its range, a leading dimension below its row's length, a
- *   negative stride, results of two groups that overlap, a NULL operand, an
+ *   negative stride, results of two groups that overlap or lie between one
+ *   another's rows (stride_w of dW below a matrix's extent), a NULL operand, an
  *   unknown type                                          -> INVALID_ARG
  *   an operand not aligned to its elements                -> UNSUPPORTED
  *   an output overlapping an input                        -> ALIAS
@@ -35,8 +36,8 @@
  * W's (the gradient's X's and dY's) rows begin on 16 bytes (pointers, leading
  * dimensions and strides) and are whole 16-byte pieces long (K % 8 == 0, and
  * N % 8 == 0 but for trans_w = 1), with leading dimensions below 2^20; the
- * result may lie anywhere.  Everything else runs on a general kernel, at a
- * half to two thirds of their rate for large products.
+ * result may lie anywhere.  Everything else runs on a general kernel, at about
+ * half their rate for large products and gradients.
  */
 #ifndef DENSE_GEMM_ROW_AMD_GEMM_GROUPED_H
 #define DENSE_GEMM_ROW_AMD_GEMM_GROUPED_H

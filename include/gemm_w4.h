@@ -28,10 +28,13 @@
  * is not 32, 64 or 128, or K above 2^30 -> INVALID_ARG.
  *
  * Speed: products of few rows (see GEMM_W4_ROWS) read codes, activations,
- * scales and zero points in whole pieces wherever their rows begin; some 10 %
- * faster where X's rows begin on 16 bytes and K % 8 == 0, and a row's scales
- * (and zero points) are whole runs of 256 k, aligned to such a run.  Scales
- * of rows of fewer than 256 k, and leading dimensions from 2^22 on, are read by
+ * scales and zero points in whole pieces wherever their rows begin.  Fastest are
+ * rows of X that begin on 16 bytes with K % 8 == 0, and scales (and zero points) a
+ * row of which is whole runs of 256 k, aligned to such a run.  Rows of X that
+ * begin on 4 bytes take up to 30 % longer; on 2 bytes, or with K odd, 5 to 30 %
+ * longer, but 8 to 32 rows of narrow layers 1.3 to 3 times as long (16 rows, 4096 x
+ * 4096: 10 us; 4096 x 4095: 30).  Scales off their runs cost up to 15 %.  Scales of
+ * rows of fewer than 256 k, and leading dimensions from 2^22 on, are read by
  * element.
  */
 #ifndef DENSE_GEMM_ROW_AMD_GEMM_W4_H
@@ -88,7 +91,9 @@ gemm_status_t gemm_w4_dequantize(int32_t dtype, int32_t s_dtype, int64_t N, int6
  * bfloat16's range, a result is taken from sum s (q - zero point) x in 64 bits
  * instead: infinities and NaN are those of the definition, and such a result
  * takes K / 32 steps of one thread.)  With more rows the weights are
- * dequantised first, rounded to dtype, into `workspace`
+ * dequantised first, rounded to dtype (which makes results off by about a third
+ * more than their own rounding; call with up to GEMM_W4_ROWS rows at a time where
+ * that counts), into `workspace`
  * (gemm_w4_matmul_workspace_bytes bytes, 16-byte aligned, not overlapping the
  * operands; too small a one -> INVALID_ARG) and multiplied as gemm_*_bt does;
  * for fewer it may be NULL.
