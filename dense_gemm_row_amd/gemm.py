@@ -370,7 +370,10 @@ def _ld(t) -> int:
         raise ValueError("expected a 2-D tensor")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("rows must be contiguous (unit column stride)")
-    return max(int(t.stride(0)), 1) if t.shape[0] > 1 else max(int(t.shape[1]), 1)
+    rows, cols = t.shape
+    if rows > 1 and cols > 0:
+        return int(t.stride(0))  # (0 for an expanded column: the library refuses it)
+    return max(int(cols), 1)
 
 
 def matmul(a, b, out=None, config: GemmConfig | None = None, stream=None, split_k: bool = True,

@@ -83,7 +83,8 @@ def _stack(w, name):
     sg, sr, sc = w.stride()
     if cols > 1 and sc != 1:
         raise ValueError(f"{name}: rows must be contiguous (unit column stride)")
-    return dtype, groups, rows, cols, max(sr if rows > 1 else cols, 1), sg if groups > 1 else rows * max(cols, 1)
+    # (As mx._dense.)
+    return dtype, groups, rows, cols, sr if rows > 1 and cols > 0 else max(cols, 1), sg if groups > 1 else rows * max(cols, 1)
 
 
 def _offsets(offsets, groups, like):

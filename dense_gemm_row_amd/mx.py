@@ -213,7 +213,8 @@ def _dense(t, name):
     sr, sc = t.stride()
     if cols > 1 and sc != 1:
         raise ValueError("rows must be contiguous (unit column stride)")
-    return dtype, rows, cols, max(sr if rows > 1 else cols, 1)
+    # (An expanded column's stride, 0, stays: the library refuses it.)
+    return dtype, rows, cols, sr if rows > 1 and cols > 0 else max(cols, 1)
 
 
 def _coded(q, name, fmt):
